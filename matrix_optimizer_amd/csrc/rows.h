@@ -1,0 +1,184 @@
+// Device helpers of the row operators (gfx950, wave64): eight consecutive
+// columns of a row per lane, the dropout generator, 8-bit rounding.
+#pragma once
+#include "block.h"
+#include "common.h"
+
+namespace muon {
+
+// 16- and 8-byte vectors at any element's alignment: rows of odd strides
+// start anywhere, and gfx950's global loads and stores take such addresses in
+// one instruction.
+typedef unsigned int u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef unsigned int u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+
+__device__ __forceinline__ void unpack8(const u32x4& v, float* f) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    f[2 * q] = __uint_as_float(v[q] << 16);
+    f[2 * q + 1] = __uint_as_float(v[q] & 0xffff0000u);
+  }
+}
+
+// Columns c .. c+7 of a row as fp32, zeros from column `cols` on.
+__device__ __forceinline__ void load8(const bf16_t* row, int64_t c, int64_t cols, float* f) {
+  if (c + 8 <= cols) {
+    const u32x4 v = *reinterpret_cast<const u32x4_any*>(row + c);
+    unpack8(v, f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = c + j < cols ? bf2f(row[c + j]) : 0.f;
+  }
+}
+__device__ __forceinline__ void load8(const float* row, int64_t c, int64_t cols, float* f) {
+  if (c + 8 <= cols) {
+    const u32x4 a = *reinterpret_cast<const u32x4_any*>(row + c), b = *reinterpret_cast<const u32x4_any*>(row + c + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[j] = __uint_as_float(a[j]);
+      f[j + 4] = __uint_as_float(b[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = c + j < cols ? row[c + j] : 0.f;
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  return (uint32_t)f2bf(lo) | ((uint32_t)f2bf(hi) << 16);
+}
+
+// The same columns rounded and stored; those from `cols` on are left alone.
+__device__ __forceinline__ void store8(bf16_t* row, int64_t c, int64_t cols, const float* f) {
+  if (c + 8 <= cols) {
+    u32x4 v;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = pack_bf16(f[2 * q], f[2 * q + 1]);
+    *reinterpret_cast<u32x4_any*>(row + c) = v;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < cols) row[c + j] = f2bf(f[j]);
+  }
+}
+__device__ __forceinline__ void store8(float* row, int64_t c, int64_t cols, const float* f) {
+  if (c + 8 <= cols) {
+    u32x4 a, b;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      a[j] = __float_as_uint(f[j]);
+      b[j] = __float_as_uint(f[j + 4]);
+    }
+    *reinterpret_cast<u32x4_any*>(row + c) = a;
+    *reinterpret_cast<u32x4_any*>(row + c + 4) = b;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < cols) row[c + j] = f[j];
+  }
+}
+
+// Limited to +-top; a NaN stays one.
+__device__ __forceinline__ float limit(float v, float top) { return v > top ? top : (v < -top ? -top : v); }
+
+// Eight values (already divided by their scale) in an 8-bit format, rounded
+// to nearest even.
+template <bool E5M2>
+__device__ __forceinline__ void store8_8bit(uint8_t* row, int64_t c, int64_t cols, const float* f) {
+  constexpr float top = E5M2 ? 57344.f : 448.f;
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = limit(f[j], top);
+  u32x2_any w;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    int p = 0;
+    if constexpr (E5M2) {
+      p = __builtin_amdgcn_cvt_pk_bf8_f32(v[4 * q], v[4 * q + 1], p, false);
+      p = __builtin_amdgcn_cvt_pk_bf8_f32(v[4 * q + 2], v[4 * q + 3], p, true);
+    } else {
+      p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * q], v[4 * q + 1], p, false);
+      p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * q + 2], v[4 * q + 3], p, true);
+    }
+    w[q] = (uint32_t)p;
+  }
+  if (c + 8 <= cols) {
+    *reinterpret_cast<u32x2_any*>(row + c) = w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < cols) row[c + j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
+  }
+}
+
+// Ten rounds of Philox4x32 (Salmon et al., 2011).
+__device__ __forceinline__ void philox(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0, uint32_t k1,
+                                       uint32_t* out) {
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c1 = (uint32_t)b;
+    c3 = (uint32_t)a;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  out[0] = c0;
+  out[1] = c1;
+  out[2] = c2;
+  out[3] = c3;
+}
+
+// Seed and offset for this launch: uniform loads where they are on the device.
+__device__ __forceinline__ void drop_seed(const Drop& d, uint64_t& seed, uint64_t& offset) {
+  seed = d.dev ? d.dev[0] : d.seed;
+  offset = d.dev ? d.dev[1] : d.offset;
+}
+
+// D on columns c .. c+7 (c a multiple of 8) of row r, in place.
+__device__ __forceinline__ void drop8(const Drop& d, uint64_t seed, uint64_t offset, int64_t r, int64_t c, float* f) {
+  uint32_t w[4];
+  philox((uint32_t)(c >> 3), (uint32_t)r, (uint32_t)offset, (uint32_t)(offset >> 32), (uint32_t)seed,
+         (uint32_t)(seed >> 32), w);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    f[2 * q] = (w[q] & 0xffffu) >= d.t ? f[2 * q] * d.up : 0.f;
+    f[2 * q + 1] = (w[q] >> 16) >= d.t ? f[2 * q + 1] * d.up : 0.f;
+  }
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, WAVE));
+  return v;
+}
+
+// Sum / maximum over the workgroup's WAVES waves, in wave order; `lds` holds
+// WAVES floats and may be reused after the call.
+template <int WAVES>
+__device__ __forceinline__ float group_sum(float v, float* lds) {
+  v = wave_sum(v);
+  if constexpr (WAVES == 1) return v;
+  if ((threadIdx.x & (WAVE - 1)) == 0) lds[threadIdx.x / WAVE] = v;
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) s += lds[w];
+  __syncthreads();
+  return s;
+}
+template <int WAVES>
+__device__ __forceinline__ float group_max(float v, float* lds) {
+  v = wave_max(v);
+  if constexpr (WAVES == 1) return v;
+  if ((threadIdx.x & (WAVE - 1)) == 0) lds[threadIdx.x / WAVE] = v;
+  __syncthreads();
+  float s = lds[0];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) s = fmaxf(s, lds[w]);
+  __syncthreads();
+  return s;
+}
+
+}  // namespace muon
