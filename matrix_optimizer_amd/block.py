@@ -136,58 +136,84 @@ class Route:
                                int(bool(self.renormalise)), self.scale)
 
 
+# The raw stream of a device's current stream; a Stream object costs 2 us to make.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _Call:
-    """Checks one call's tensors against each other; the first fixes the device."""
+    """Checks one call's tensors against its first, a [rows, cols] matrix, whose shape, type and device the
+    others share unless they say otherwise.  Small calls are bound by this code: few steps, no formatting
+    before something is wrong."""
+    __slots__ = ("where", "shape", "dtype", "index")
 
     def __init__(self, where: str, first):
-        self.where, self.device = where, first.device
-        if not first.is_cuda:
-            raise ValueError(f"{where}: device tensors are needed, got one on {first.device}")
+        self.where, self.shape, self.dtype, self.index = where, first.shape, first.dtype, first.get_device()
 
-    def fail(self, name, what):
-        raise ValueError(f"{self.where}: {name} {what}")
+    def rows(self):
+        """(rows, cols, dtype code) of the first tensor."""
+        if len(self.shape) != 2:
+            raise ValueError(f"{self.where}: [rows, cols] is needed, got {list(self.shape)}")
+        if self.dtype not in _DTYPES:
+            raise TypeError(f"{self.where}: unsupported dtype {self.dtype}")
+        self.on_device()
+        return self.shape[0], self.shape[1], _DTYPES[self.dtype]
 
-    def matrix(self, name, t, rows, cols, dtype):
-        """(address, row stride) of a [rows, cols] tensor, (None, 0) for None."""
+    def on_device(self):
+        if self.index < 0:
+            raise ValueError(f"{self.where}: device tensors are needed")
+
+    def wrong(self, name, t, shape, dtypes):
+        if t.shape != shape:
+            raise ValueError(f"{self.where}: {name} must be {list(shape)}, got {list(t.shape)}")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{self.where}: {name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+        if t.get_device() != self.index:
+            raise ValueError(f"{self.where}: {name} is on {t.device}, not on device {self.index}")
+        raise ValueError(f"{self.where}: {name} must be contiguous{' along its rows' if t.dim() == 2 else ''}")
+
+    def matrix(self, name, t, dtype=None):
+        """(address, row stride) of a matrix like the first, (None, 0) for None.  The stride of a single row
+        is not read."""
         if t is None:
             return None, 0
-        if t.shape != (rows, cols):
-            self.fail(name, f"must be [{rows}, {cols}], got {list(t.shape)}")
-        if t.dtype != dtype:
-            self.fail(name, f"must be {dtype}, got {t.dtype}")
-        if t.device != self.device:
-            self.fail(name, f"is on {t.device}, not {self.device}")
-        s = t.stride()
-        if s[1] != 1 and cols > 1:
-            self.fail(name, "must be contiguous along its rows")
-        return t.data_ptr(), (s[0] if rows > 1 else cols)
+        dtype = dtype or self.dtype
+        stride = t.stride()
+        if t.shape != self.shape or t.dtype is not dtype or t.get_device() != self.index \
+                or (stride[1] != 1 and self.shape[1] > 1):
+            self.wrong(name, t, self.shape, (dtype,))
+        return t.data_ptr(), stride[0]
 
     def flat(self, name, t, shape, dtypes):
         """Address of a contiguous tensor of one of `dtypes`, None for None."""
         if t is None:
             return None
-        if t.shape != shape:
-            self.fail(name, f"must be {list(shape)}, got {list(t.shape)}")
-        if t.dtype not in dtypes:
-            self.fail(name, f"has type {t.dtype}")
-        if t.device != self.device:
-            self.fail(name, f"is on {t.device}, not {self.device}")
-        if not t.is_contiguous():
-            self.fail(name, "must be contiguous")
+        if t.shape != shape or t.dtype not in dtypes or t.get_device() != self.index or not t.is_contiguous():
+            self.wrong(name, t, shape, dtypes)
         return t.data_ptr()
 
     def workspace(self, t):
         if t is None:
             return None, 0
-        if t.device != self.device or not t.is_contiguous():
-            self.fail("workspace", "must be a contiguous tensor on the same device")
+        if t.get_device() != self.index or not t.is_contiguous():
+            raise ValueError(f"{self.where}: workspace must be a contiguous tensor on device {self.index}")
         return t.data_ptr(), t.numel() * t.element_size()
 
-    def run(self, fn, *args, stream=None):
+    def dropout(self, d):
+        """(what keeps the C struct alive, its address)."""
+        if d is None:
+            return None, None
+        if d.device is not None and d.device.get_device() != self.index:
+            raise ValueError(f"{self.where}: Dropout.device is on {d.device.device}, not on device {self.index}")
+        c = d.to_c()
+        return c, C.addressof(c)
+
+    def run(self, fn, *args, stream):
+        index = self.index
         if stream is None:
-            stream = torch.cuda.current_stream(self.device).cuda_stream
-        if self.device.index != torch.cuda.current_device():
-            with torch.cuda.device(self.device):
+            stream = _raw_stream(index)
+        if index != torch.cuda.current_device():
+            with torch.cuda.device(index):
                 st = fn(*args, stream)
         else:
             st = fn(*args, stream)
@@ -201,21 +227,12 @@ _WEIGHT = (torch.float32, torch.bfloat16)
 _BYTE = (torch.uint8, torch.bool)
 
 
-def _rows_of(where, t, name):
-    if t.dim() != 2:
-        raise ValueError(f"{where}: {name} must be [rows, cols], got {list(t.shape)}")
-    if t.dtype not in _DTYPES:
-        raise TypeError(f"{where}: unsupported dtype {t.dtype}")
-    return t.shape[0], t.shape[1], t.dtype
-
-
 def muon_dropout(x, y, dropout: Dropout, stream=None) -> None:
     """y = D(x); y may be x.  The backward pass is the same call on the gradient."""
-    rows, cols, dt = _rows_of("muon_dropout", x, "x")
     c = _Call("muon_dropout", x)
-    xp, xs = c.matrix("x", x, rows, cols, dt)
-    yp, ys = c.matrix("y", y, rows, cols, dt)
-    c.run(lib().muon_dropout, rows, cols, xp, xs, yp, ys, _DTYPES[dt], C.byref(dropout.to_c()), stream=stream)
+    rows, cols, dt = c.rows()
+    keep, spec = c.dropout(dropout)
+    c.run(lib().muon_dropout, rows, cols, *c.matrix("x", x), *c.matrix("y", y), dt, spec, stream=stream)
 
 
 def muon_norm_forward(x, y, residual=None, h=None, weight=None, rstd=None, scales=None, group: int = 0,
@@ -223,20 +240,18 @@ def muon_norm_forward(x, y, residual=None, h=None, weight=None, rstd=None, scale
     """z = residual + D(x); h = z; y = z rstd weight (muon_norm_forward).  x, residual, h: one type (fp32 or
     bf16); y: fp32, bf16, float8_e4m3fn or float8_e5m2, the latter two with scales [rows, groups] fp32 (groups
     of `group` columns, 0 = the row).  h may be x or residual."""
-    where = "muon_norm_forward"
-    rows, cols, dt = _rows_of(where, x, "x")
-    c = _Call(where, x)
+    c = _Call("muon_norm_forward", x)
+    rows, cols, dt = c.rows()
     if y.dtype not in _ROW_DTYPES:
-        raise TypeError(f"{where}: unsupported dtype {y.dtype}")
-    a = muon_norm_args(rows, cols, *c.matrix("x", x, rows, cols, dt), *c.matrix("residual", residual, rows, cols, dt),
-                       *c.matrix("h", h, rows, cols, dt), *c.matrix("y", y, rows, cols, y.dtype),
-                       c.flat("weight", weight, (cols,), _WEIGHT),
-                       *c.matrix("scales", scales, rows, -(-cols // group) if group > 0 else 1, torch.float32),
-                       c.flat("rstd", rstd, (rows,), _F32), None, _DTYPES[dt],
-                       0 if weight is None else _DTYPES[weight.dtype], _ROW_DTYPES[y.dtype], group, eps)
-    if dropout is not None:
-        d = dropout.to_c()
-        a.dropout = C.addressof(d)
+        raise TypeError(f"muon_norm_forward: unsupported dtype {y.dtype}")
+    keep, spec = c.dropout(dropout)
+    groups = 0
+    if scales is not None:
+        groups = -(-cols // group) if group > 0 else 1
+    a = muon_norm_args(rows, cols, *c.matrix("x", x), *c.matrix("residual", residual), *c.matrix("h", h),
+                       *c.matrix("y", y, y.dtype), c.flat("weight", weight, (cols,), _WEIGHT),
+                       c.flat("scales", scales, (rows, groups), _F32), groups, c.flat("rstd", rstd, (rows,), _F32),
+                       spec, dt, 0 if weight is None else _DTYPES[weight.dtype], _ROW_DTYPES[y.dtype], group, eps)
     c.run(lib().muon_norm_forward, C.byref(a), stream=stream)
 
 
@@ -251,17 +266,14 @@ def muon_norm_backward(dy, h, rstd, weight=None, dh=None, dresidual=None, dx=Non
     """The gradients of muon_norm_forward from its h and rstd: dresidual = dz, dx = D(dz), dweight (fp32, with
     a uint8 workspace of norm_workspace_bytes).  dh: the gradient arriving on the residual stream; dresidual
     may be dh."""
-    where = "muon_norm_backward"
-    rows, cols, dt = _rows_of(where, dy, "dy")
-    c = _Call(where, dy)
-    a = muon_norm_grad_args(rows, cols, *c.matrix("dy", dy, rows, cols, dt), *c.matrix("h", h, rows, cols, dt),
-                            *c.matrix("dh", dh, rows, cols, dt), *c.matrix("dresidual", dresidual, rows, cols, dt),
-                            *c.matrix("dx", dx, rows, cols, dt), c.flat("rstd", rstd, (rows,), _F32),
-                            c.flat("weight", weight, (cols,), _WEIGHT), c.flat("dweight", dweight, (cols,), _F32),
-                            None, _DTYPES[dt], 0 if weight is None else _DTYPES[weight.dtype])
-    if dropout is not None:
-        d = dropout.to_c()
-        a.dropout = C.addressof(d)
+    c = _Call("muon_norm_backward", dy)
+    rows, cols, dt = c.rows()
+    keep, spec = c.dropout(dropout)
+    a = muon_norm_grad_args(rows, cols, *c.matrix("dy", dy), *c.matrix("h", h), *c.matrix("dh", dh),
+                            *c.matrix("dresidual", dresidual), *c.matrix("dx", dx),
+                            c.flat("rstd", rstd, (rows,), _F32), c.flat("weight", weight, (cols,), _WEIGHT),
+                            c.flat("dweight", dweight, (cols,), _F32), spec, dt,
+                            0 if weight is None else _DTYPES[weight.dtype])
     c.run(lib().muon_norm_backward, C.byref(a), *c.workspace(workspace), stream=stream)
 
 
@@ -270,28 +282,23 @@ def muon_route_forward(route: Route, logits, experts, weights, bias=None, token_
     """experts [rows, top_k] int32 and weights fp32 of each row's logits [rows, E] (fp32 or bf16).  bias: fp32
     [E], moves the choice only; token_mask: bool or uint8 [rows], rows of 0 choose nothing (-1); scores: fp32
     [rows, E], optional output."""
-    where = "muon_route_forward"
-    rows, n, dt = _rows_of(where, logits, "logits")
-    c = _Call(where, logits)
-    k = route.top_k
-    a = muon_route_args(rows, n, *c.matrix("logits", logits, rows, n, dt), c.flat("bias", bias, (n,), _F32),
-                        c.flat("token_mask", token_mask, (rows,), _BYTE),
-                        c.flat("experts", experts, (rows, k), _I32), c.flat("weights", weights, (rows, k), _F32),
-                        c.flat("scores", scores, (rows, n), _F32), _DTYPES[dt])
+    c = _Call("muon_route_forward", logits)
+    rows, n, dt = c.rows()
+    pairs = (rows, route.top_k)
+    a = muon_route_args(rows, n, *c.matrix("logits", logits), c.flat("bias", bias, (n,), _F32),
+                        c.flat("token_mask", token_mask, (rows,), _BYTE), c.flat("experts", experts, pairs, _I32),
+                        c.flat("weights", weights, pairs, _F32), c.flat("scores", scores, (rows, n), _F32), dt)
     c.run(lib().muon_route_forward, C.byref(route.to_c()), C.byref(a), stream=stream)
 
 
 def muon_route_backward(route: Route, logits, experts, weights, dweights, dlogits, dscores=None, stream=None) -> None:
     """dlogits (logits' type, all written) from dweights, and dscores where the scores were used."""
-    where = "muon_route_backward"
-    rows, n, dt = _rows_of(where, logits, "logits")
-    c = _Call(where, logits)
-    k = route.top_k
-    a = muon_route_grad_args(rows, n, *c.matrix("logits", logits, rows, n, dt),
-                             c.flat("experts", experts, (rows, k), _I32), c.flat("weights", weights, (rows, k), _F32),
-                             c.flat("dweights", dweights, (rows, k), _F32),
-                             c.flat("dscores", dscores, (rows, n), _F32),
-                             *c.matrix("dlogits", dlogits, rows, n, dt), _DTYPES[dt])
+    c = _Call("muon_route_backward", logits)
+    rows, n, dt = c.rows()
+    pairs = (rows, route.top_k)
+    a = muon_route_grad_args(rows, n, *c.matrix("logits", logits), c.flat("experts", experts, pairs, _I32),
+                             c.flat("weights", weights, pairs, _F32), c.flat("dweights", dweights, pairs, _F32),
+                             c.flat("dscores", dscores, (rows, n), _F32), *c.matrix("dlogits", dlogits), dt)
     c.run(lib().muon_route_backward, C.byref(route.to_c()), C.byref(a), stream=stream)
 
 
@@ -305,19 +312,19 @@ def route_order_workspace_bytes(num_pairs: int, num_experts: int) -> int:
 def muon_route_order(experts, counts, offsets, order, position, workspace, stream=None) -> None:
     """The pairs of `experts` (int32, any shape) grouped by expert: counts [E], offsets [E + 1], order [pairs],
     position (experts' shape), all int32; workspace: uint8 of route_order_workspace_bytes."""
-    where = "muon_route_order"
-    c = _Call(where, experts)
+    c = _Call("muon_route_order", experts)
+    c.on_device()
     n, pairs = counts.numel(), experts.numel()
-    ws, wb = c.workspace(workspace)
-    c.run(lib().muon_route_order, pairs, n, c.flat("experts", experts, experts.shape, _I32),
+    c.run(lib().muon_route_order, pairs, n, c.flat("experts", experts, c.shape, _I32),
           c.flat("counts", counts, (n,), _I32), c.flat("offsets", offsets, (n + 1,), _I32),
-          c.flat("order", order, (pairs,), _I32), c.flat("position", position, experts.shape, _I32), ws, wb,
-          stream=stream)
+          c.flat("order", order, (pairs,), _I32), c.flat("position", position, c.shape, _I32),
+          *c.workspace(workspace), stream=stream)
 
 
 def muon_route_balance(counts, bias, out, rate: float, stream=None) -> None:
     """out = bias + rate sign(mean(counts) - counts); out may be bias."""
     c = _Call("muon_route_balance", counts)
+    c.on_device()
     n = counts.numel()
     c.run(lib().muon_route_balance, n, c.flat("counts", counts, (n,), _I32), c.flat("bias", bias, (n,), _F32),
           c.flat("out", out, (n,), _F32), rate, stream=stream)

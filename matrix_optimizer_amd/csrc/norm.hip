@@ -13,7 +13,6 @@ namespace muon {
 namespace {
 
 constexpr int NT = 256;            // threads of a workgroup
-constexpr int NW = NT / WAVE;
 constexpr int64_t kMaxGrid = 1 << 16;
 
 // D(x) alone: eight columns a lane.  `per_row` = chunks of eight in a row.
@@ -64,7 +63,9 @@ __device__ __forceinline__ float scale_of(float most, float top) {
 }
 
 // y of columns c .. c+7 at its type; an 8-bit y with the group's scale, found
-// across the group's lanes unless the row's is given.
+// across the group's lanes unless the row's is given.  LPR: lanes of a row if
+// fewer than a wave (a group then ends with the row).
+template <int LPR>
 __device__ __forceinline__ void store_y(const muon_norm_args& a, int64_t r, int64_t c, float* y, float row_scale) {
   if (a.y_dtype == MUON_ROW_F32) {
     if (c < a.cols) store8(static_cast<float*>(a.y) + r * a.y_stride, c, a.cols, y);
@@ -77,7 +78,7 @@ __device__ __forceinline__ void store_y(const muon_norm_args& a, int64_t r, int6
       float most = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(y[j]));
-      for (int o = a.group / 16; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, WAVE));
+      for (int o = LPR ? min(a.group / 16, LPR / 2) : a.group / 16; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, WAVE));
       scale = scale_of(most, e5 ? 57344.f : 448.f);
       if (c < a.cols && (c & (a.group - 1)) == 0) a.scales[r * a.scales_stride + c / a.group] = scale;
     }
@@ -92,41 +93,163 @@ __device__ __forceinline__ void store_y(const muon_norm_args& a, int64_t r, int6
   }
 }
 
-// One workgroup a row, z formed again in each pass over it.
-template <typename T>
-__global__ __launch_bounds__(NT) void norm_fwd(muon_norm_args a, Drop d) {
-  __shared__ float lds[NW];
+// The 8-bit scale of a whole row is one more reduction.
+__device__ __forceinline__ bool row_scaled(const muon_norm_args& a) {
+  return a.y_dtype >= MUON_ROW_E4M3 && a.group == 0;
+}
+__device__ __forceinline__ float fmax_of(int y_dtype) { return y_dtype == MUON_ROW_E5M2 ? 57344.f : 448.f; }
+
+// Sum / maximum over LPR neighbouring lanes.
+template <int LPR>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = LPR / 2; o >= 1; o >>= 1) v += __shfl_xor(v, o, WAVE);
+  return v;
+}
+template <int LPR>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int o = LPR / 2; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, WAVE));
+  return v;
+}
+
+// Where a lane stands: `lanes` lanes share a row, this is the t-th of them;
+// rows r, r + step, ... are theirs.
+template <int LPR>
+struct RowLanes {
+  int lanes, t;
+  int64_t r, step;
+  __device__ __forceinline__ RowLanes() {
+    lanes = LPR ? LPR : (int)blockDim.x;
+    t = LPR ? threadIdx.x & (LPR - 1) : threadIdx.x;
+    constexpr int rows = LPR ? NT / (LPR ? LPR : 1) : 1;   // of a workgroup at a time
+    r = blockIdx.x * (int64_t)rows + (LPR ? threadIdx.x / (LPR ? LPR : 1) : 0);
+    step = (int64_t)gridDim.x * rows;
+  }
+};
+
+// The row in registers: every lane keeps NC chunks of eight columns, `lanes`
+// chunks apart, so each input is read once.  LPR = 8 .. 64 lanes a row and no
+// barriers up to 1024 columns, else (LPR = 0) a workgroup of up to 512 lanes a
+// row.  The workgroups stay and step over the rows; the next row's loads are
+// issued before this row's reduction and stores, so that memory is busy
+// meanwhile.
+template <typename T, int NC, int LPR>
+__global__ __launch_bounds__(LPR ? NT : 512) void norm_fwd(muon_norm_args a, Drop d) {
+  __shared__ GroupRed sums, maxima;
+  if constexpr (LPR == 0) {
+    red_init(sums);
+    red_init(maxima);
+  }
+  const RowLanes<LPR> at;
+  const int lanes = at.lanes, t = at.t;
+  const int64_t step = at.step;
+  int64_t r = at.r;
   uint64_t seed, offset;
   drop_seed(d, seed, offset);
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+  const T* x = static_cast<const T*>(a.x);
+  const T* res = static_cast<const T*>(a.residual);
+  float w[NC][8];
+  Chunk<T> cx[NC], cr[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int64_t c = (int64_t)(i * lanes + t) * 8;
+    weight8(a.weight, a.weight_dtype, c, a.cols, w[i]);
+    if (r < a.rows) {
+      cx[i].load(x + r * a.x_stride, c, a.cols);
+      if (res) cr[i].load(res + r * a.residual_stride, c, a.cols);
+    }
+  }
+  for (int turn = 0; r < a.rows; r += step, turn ^= 1) {
+    float z[NC][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int64_t c = (int64_t)(i * lanes + t) * 8;
+      cx[i].get(z[i]);
+      if (d.on) drop8(d, seed, offset, r, c, z[i]);
+      if (res) {
+        float e[8];
+        cr[i].get(e);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[i][j] += e[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss += z[i][j] * z[i][j];
+    }
+    if (r + step < a.rows) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int64_t c = (int64_t)(i * lanes + t) * 8;
+        cx[i].load(x + (r + step) * a.x_stride, c, a.cols);
+        if (res) cr[i].load(res + (r + step) * a.residual_stride, c, a.cols);
+      }
+    }
+    ss = LPR ? lanes_sum<LPR>(ss) : group_sum(ss, sums, turn);
+    const float rstd = 1.f / sqrtf(ss / (float)a.cols + a.eps);
+    if (a.rstd && t == 0) a.rstd[r] = rstd;
+    if (a.h) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int64_t c = (int64_t)(i * lanes + t) * 8;
+        if (c < a.cols) store8(static_cast<T*>(a.h) + r * a.h_stride, c, a.cols, z[i]);
+      }
+    }
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        z[i][j] = z[i][j] * rstd * w[i][j];   // past the row's end 0, or NaN with rstd: fmaxf passes over it
+        most = fmaxf(most, fabsf(z[i][j]));
+      }
+    float row_scale = 1.f;
+    if (row_scaled(a)) {
+      most = LPR ? lanes_max<LPR>(most) : group_max(most, maxima, turn);
+      row_scale = scale_of(most, fmax_of(a.y_dtype));
+      if (t == 0) a.scales[r * a.scales_stride] = row_scale;
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) store_y<LPR>(a, r, (int64_t)(i * lanes + t) * 8, z[i], row_scale);
+  }
+}
+
+// Rows longer than the registers hold: z is formed again in each pass over
+// the row, which the caches mostly hold by then.
+template <typename T>
+__global__ __launch_bounds__(512) void norm_fwd_long(muon_norm_args a, Drop d) {
+  __shared__ GroupRed sums, maxima;
+  red_init(sums);
+  red_init(maxima);
+  uint64_t seed, offset;
+  drop_seed(d, seed, offset);
+  const int64_t pass = (int64_t)blockDim.x * 8;
+  int turn = 0;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
     float z[8], w[8];
     float ss = 0.f;
-    for (int64_t c0 = 0; c0 < a.cols; c0 += NT * 8) {
-      const int64_t c = c0 + threadIdx.x * 8;
-      if (c >= a.cols) continue;
+    for (int64_t c = threadIdx.x * 8; c < a.cols; c += pass) {
       z8<T>(a, d, seed, offset, r, c, z);
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss += z[j] * z[j];
     }
-    ss = group_sum<NW>(ss, lds);
+    ss = group_sum(ss, sums, turn);
     const float rstd = 1.f / sqrtf(ss / (float)a.cols + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd;
     float row_scale = 1.f;
-    if (a.y_dtype >= MUON_ROW_E4M3 && a.group == 0) {
+    if (row_scaled(a)) {
       float most = 0.f;
-      for (int64_t c0 = 0; c0 < a.cols; c0 += NT * 8) {
-        const int64_t c = c0 + threadIdx.x * 8;
-        if (c >= a.cols) continue;
+      for (int64_t c = threadIdx.x * 8; c < a.cols; c += pass) {
         z8<T>(a, d, seed, offset, r, c, z);
         weight8(a.weight, a.weight_dtype, c, a.cols, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) most = fmaxf(most, c + j < a.cols ? fabsf(z[j] * rstd * w[j]) : 0.f);
       }
-      most = group_max<NW>(most, lds);
-      row_scale = scale_of(most, a.y_dtype == MUON_ROW_E5M2 ? 57344.f : 448.f);
+      most = group_max(most, maxima, turn);
+      row_scale = scale_of(most, fmax_of(a.y_dtype));
       if (threadIdx.x == 0) a.scales[r * a.scales_stride] = row_scale;
     }
-    for (int64_t c0 = 0; c0 < a.cols; c0 += NT * 8) {
+    for (int64_t c0 = 0; c0 < a.cols; c0 += pass) {
       const int64_t c = c0 + threadIdx.x * 8;   // lanes past the row's end take part in their group's maximum
       float y[8];
       const bool in = c < a.cols;
@@ -137,31 +260,158 @@ __global__ __launch_bounds__(NT) void norm_fwd(muon_norm_args a, Drop d) {
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) y[j] = in && c + j < a.cols ? z[j] * rstd * w[j] : 0.f;
-      store_y(a, r, c, y, row_scale);
+      store_y<0>(a, r, c, y, row_scale);
     }
   }
 }
 
-template <typename T>
-__global__ __launch_bounds__(NT) void norm_bwd(muon_norm_grad_args a, Drop d) {
-  __shared__ float lds[NW];
+// Backward, the row in registers as in norm_fwd.  dweight's sums stay in the
+// lanes' registers over all of a workgroup's rows; each workgroup leaves one
+// row of partial sums (or the result, if it is the only one).
+template <typename T, int NC, int LPR>
+__global__ __launch_bounds__(LPR ? NT : 512) void norm_bwd(muon_norm_grad_args a, Drop d, float* parts) {
+  __shared__ GroupRed sums;
+  if constexpr (LPR == 0) red_init(sums);
+  const RowLanes<LPR> at;
+  const int lanes = at.lanes, t = at.t;
+  const int64_t step = at.step;
+  int64_t r = at.r;
   uint64_t seed, offset;
   drop_seed(d, seed, offset);
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+  const T* dy = static_cast<const T*>(a.dy);
+  const T* h = static_cast<const T*>(a.h);
+  const T* dh = static_cast<const T*>(a.dh);
+  float w[NC][8], dw[NC][8];
+  // four chunks a lane leave no registers for the next row's
+  constexpr bool AHEAD = NC <= 2;
+  Chunk<T> cg[NC], ch[NC], cd[NC];
+  float rstd = 0.f;
+  auto fetch = [&](int64_t row) {
+    rstd = a.rstd[row];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int64_t c = (int64_t)(i * lanes + t) * 8;
+      cg[i].load(dy + row * a.dy_stride, c, a.cols);
+      ch[i].load(h + row * a.h_stride, c, a.cols);
+      if (dh) cd[i].load(dh + row * a.dh_stride, c, a.cols);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    weight8(a.weight, a.weight_dtype, (int64_t)(i * lanes + t) * 8, a.cols, w[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+  }
+  if (AHEAD && r < a.rows) fetch(r);
+  for (int turn = 0; r < a.rows; r += step, turn ^= 1) {
+    if (!AHEAD) fetch(r);
+    float g[NC][8], xh[NC][8];
+    Chunk<T> e[NC];
+    float dot = 0.f;
+    const float rs = rstd;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      cg[i].get(g[i]);
+      ch[i].get(xh[i]);
+      e[i] = cd[i];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        xh[i][j] *= rs;
+        dw[i][j] += g[i][j] * xh[i][j];
+        g[i][j] *= w[i][j];
+        dot += g[i][j] * xh[i][j];
+      }
+    }
+    if (AHEAD && r + step < a.rows) fetch(r + step);
+    const float mean = (LPR ? lanes_sum<LPR>(dot) : group_sum(dot, sums, turn)) / (float)a.cols;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int64_t c = (int64_t)(i * lanes + t) * 8;
+      if (c >= a.cols) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[i][j] = rs * (g[i][j] - xh[i][j] * mean);
+      if (dh) {
+        float f[8];
+        e[i].get(f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[i][j] += f[j];
+      }
+      if (a.dresidual) store8(static_cast<T*>(a.dresidual) + r * a.dresidual_stride, c, a.cols, g[i]);
+      if (a.dx) {
+        if (d.on) drop8(d, seed, offset, r, c, g[i]);
+        store8(static_cast<T*>(a.dx) + r * a.dx_stride, c, a.cols, g[i]);
+      }
+    }
+  }
+  if (!a.dweight) return;
+  float* out = gridDim.x == 1 ? a.dweight : parts + blockIdx.x * a.cols;
+  if constexpr (LPR != 0) {
+    // the rows a workgroup worked on side by side, added in their order
+    constexpr int rows = NT / (LPR ? LPR : 1);
+    __shared__ float all[rows][NC * 8][LPR];
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) all[threadIdx.x / LPR][i * 8 + j][t] = dw[i][j];
+    __syncthreads();
+    for (int q = threadIdx.x; q < NC * 8 * LPR; q += NT) {
+      const int k = q / LPR, lane = q % LPR;   // chunk k / 8 of that lane, its column k % 8
+      const int64_t c = (int64_t)((k / 8) * LPR + lane) * 8 + k % 8;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < rows; ++w) v += all[w][k][lane];
+      if (c < a.cols) out[c] = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int64_t c = (int64_t)(i * lanes + t) * 8;
+      if (c < a.cols) store8(out, c, a.cols, dw[i]);
+    }
+  }
+}
+
+// Rows longer than the registers hold: two passes over the row, and dweight's
+// partial sums (a row of `parts` for each workgroup, its own lanes' columns) in memory.
+template <typename T>
+__global__ __launch_bounds__(512) void norm_bwd_long(muon_norm_grad_args a, Drop d, float* parts) {
+  __shared__ GroupRed sums;
+  red_init(sums);
+  uint64_t seed, offset;
+  drop_seed(d, seed, offset);
+  const int64_t pass = (int64_t)blockDim.x * 8;
+  float* out = gridDim.x == 1 ? a.dweight : parts + blockIdx.x * a.cols;
+  int turn = 0;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
     const T* dy_r = static_cast<const T*>(a.dy) + r * a.dy_stride;
     const T* h_r = static_cast<const T*>(a.h) + r * a.h_stride;
     const float rstd = a.rstd[r];
     float g[8], h[8], w[8];
     float dot = 0.f;
-    for (int64_t c = threadIdx.x * 8; c < a.cols; c += NT * 8) {
+    for (int64_t c = threadIdx.x * 8; c < a.cols; c += pass) {
       load8(dy_r, c, a.cols, g);
       load8(h_r, c, a.cols, h);
       weight8(a.weight, a.weight_dtype, c, a.cols, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dot += g[j] * w[j] * (h[j] * rstd);
+      for (int j = 0; j < 8; ++j) {
+        h[j] *= rstd;
+        dot += g[j] * w[j] * h[j];
+      }
+      if (a.dweight) {
+        float s[8];
+        if (r == (int64_t)blockIdx.x) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[j] = 0.f;
+        } else {
+          load8(out, c, a.cols, s);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] += g[j] * h[j];
+        store8(out, c, a.cols, s);
+      }
     }
-    const float mean = group_sum<NW>(dot, lds) / (float)a.cols;
-    for (int64_t c = threadIdx.x * 8; c < a.cols; c += NT * 8) {
+    const float mean = group_sum(dot, sums, turn) / (float)a.cols;
+    for (int64_t c = threadIdx.x * 8; c < a.cols; c += pass) {
       load8(dy_r, c, a.cols, g);
       load8(h_r, c, a.cols, h);
       weight8(a.weight, a.weight_dtype, c, a.cols, w);
@@ -181,30 +431,74 @@ __global__ __launch_bounds__(NT) void norm_bwd(muon_norm_grad_args a, Drop d) {
   }
 }
 
-// dweight in two launches: part p sums rows p, p + parts, ... of 256 columns,
-// then a thread sums its column over the parts, both in ascending order.
-template <typename T>
-__global__ __launch_bounds__(NT) void norm_dw_part(muon_norm_grad_args a, float* parts) {
-  const int64_t c = blockIdx.x * (int64_t)NT + threadIdx.x;
-  if (c >= a.cols) return;
-  float s = 0.f;
-  for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y)
-    s += ld_as_f32(static_cast<const T*>(a.dy) + r * a.dy_stride, c) *
-         (ld_as_f32(static_cast<const T*>(a.h) + r * a.h_stride, c) * a.rstd[r]);
-  parts[blockIdx.y * a.cols + c] = s;
-}
-
-__global__ __launch_bounds__(NT) void norm_dw_sum(int64_t cols, int64_t n, const float* parts, float* dw) {
-  const int64_t c = blockIdx.x * (int64_t)NT + threadIdx.x;
-  if (c >= cols) return;
-  float s = 0.f;
-  for (int64_t p = 0; p < n; ++p) s += parts[p * cols + c];
-  dw[c] = s;
+// dweight from the partial sums: a workgroup 32 columns, 32 lanes a column,
+// each every 32nd part in ascending order, then the 32 sums in order.
+constexpr int DWC = 32, DWL = 32;
+__global__ __launch_bounds__(DWC* DWL) void norm_dw_sum(int64_t cols, int64_t n, const float* parts, float* dw) {
+  __shared__ float s[DWL][DWC + 1];
+  const int cc = threadIdx.x % DWC, k = threadIdx.x / DWC;
+  const int64_t c = blockIdx.x * (int64_t)DWC + cc;
+  float v = 0.f;
+  if (c < cols) {
+    int64_t p = k;
+    for (; p + 7 * DWL < n; p += 8 * DWL) {   // eight loads in flight
+      float e[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) e[q] = parts[(p + q * DWL) * cols + c];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v += e[q];
+    }
+    for (; p < n; p += DWL) v += parts[p * cols + c];
+  }
+  s[k][cc] = v;
+  __syncthreads();
+  if (k == 0 && c < cols) {
+    v = 0.f;
+#pragma unroll
+    for (int q = 0; q < DWL; ++q) v += s[q][cc];
+    dw[c] = v;
+  }
 }
 
 }  // namespace
 
-int64_t norm_parts(int64_t rows, int64_t cols) { return rows < 512 ? rows : 512; }
+namespace {
+
+// How a row is laid over lanes: up to 1024 columns 8 to 64 lanes, up to 16384
+// a workgroup of as many waves as its chunks fill, longer rows in passes.
+struct RowShape {
+  int lpr;             // lanes a row; 0: the workgroup
+  int nc;              // chunks a lane keeps; 0: in passes
+  unsigned threads;
+  int64_t per_group;   // rows a workgroup works on at once
+};
+RowShape row_shape(int64_t cols) {
+  const int64_t chunks = (cols + 7) / 8;
+  if (chunks <= 2 * WAVE) {
+    const int lpr = chunks <= 8 ? 8 : chunks <= 16 ? 16 : chunks <= 32 ? 32 : 64;
+    return {lpr, chunks <= WAVE ? 1 : 2, NT, NT / lpr};
+  }
+  const int nc = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : chunks <= 2048 ? 4 : 0;
+  if (nc == 0) return {0, 0, 512, 1};
+  return {0, nc, (unsigned)round_up((chunks + nc - 1) / nc, WAVE), 1};
+}
+
+// Forward: workgroups that stay on the GPU, 1024 lanes on each of 256 CUs.
+// [16384, 4096] bf16 with p = 0.1: 105 us, 111 with twice as many (the last
+// round of workgroups is then part empty), 111 with half.
+int64_t resident(unsigned threads) { return 256 * std::max(1u, 1024 / threads); }
+
+}  // namespace
+
+// Backward: each workgroup leaves a row of partial sums, written and read
+// again.  Two workgroups a CU where a lane keeps one chunk ([16384, 4096] with
+// dropout: 110 us, one 117, four 124), one where it keeps more ([4096, 8192]:
+// 43 us, two 48) and where two would leave fewer than 8 rows to each.
+int64_t norm_parts(int64_t rows, int64_t cols) {
+  const RowShape s = row_shape(cols);
+  const int64_t groups = (rows + s.per_group - 1) / s.per_group;
+  return std::min<int64_t>(groups, s.nc == 1 && groups >= 4096 ? 512 : 256);
+}
 
 hipError_t run_dropout(int64_t rows, int64_t cols, const void* x, int64_t xs, void* y, int64_t ys, int dtype,
                        const Drop& d, hipStream_t stream) {
@@ -219,33 +513,56 @@ hipError_t run_dropout(int64_t rows, int64_t cols, const void* x, int64_t xs, vo
   return hipGetLastError();
 }
 
+template <typename T>
+static void launch_forward(const muon_norm_args& a, const Drop& d, hipStream_t stream) {
+  const RowShape s = row_shape(a.cols);
+  const int64_t groups = (a.rows + s.per_group - 1) / s.per_group;
+  const dim3 grid((unsigned)std::min(groups, resident(s.threads))), block(s.threads);
+  if (s.lpr == 8) MUON_LAUNCH("norm_fwd", (norm_fwd<T, 1, 8>), grid, block, stream, a, d);
+  else if (s.lpr == 16) MUON_LAUNCH("norm_fwd", (norm_fwd<T, 1, 16>), grid, block, stream, a, d);
+  else if (s.lpr == 32) MUON_LAUNCH("norm_fwd", (norm_fwd<T, 1, 32>), grid, block, stream, a, d);
+  else if (s.lpr == 64 && s.nc == 1) MUON_LAUNCH("norm_fwd", (norm_fwd<T, 1, 64>), grid, block, stream, a, d);
+  else if (s.lpr == 64) MUON_LAUNCH("norm_fwd", (norm_fwd<T, 2, 64>), grid, block, stream, a, d);
+  else if (s.nc == 1) MUON_LAUNCH("norm_fwd", (norm_fwd<T, 1, 0>), grid, block, stream, a, d);
+  else if (s.nc == 2) MUON_LAUNCH("norm_fwd", (norm_fwd<T, 2, 0>), grid, block, stream, a, d);
+  else if (s.nc == 4) MUON_LAUNCH("norm_fwd", (norm_fwd<T, 4, 0>), grid, block, stream, a, d);
+  else MUON_LAUNCH("norm_fwd_long", norm_fwd_long<T>, grid, block, stream, a, d);
+}
+
 hipError_t run_norm_forward(const muon_norm_args& a, const Drop& d, hipStream_t stream) {
-  const dim3 grid((unsigned)std::min<int64_t>(a.rows, kMaxGrid));
-  if (a.dtype == MUON_BF16) MUON_LAUNCH("norm_fwd", norm_fwd<bf16_t>, grid, dim3(NT), stream, a, d);
-  else MUON_LAUNCH("norm_fwd", norm_fwd<float>, grid, dim3(NT), stream, a, d);
+  if (a.dtype == MUON_BF16) launch_forward<bf16_t>(a, d, stream);
+  else launch_forward<float>(a, d, stream);
   return hipGetLastError();
 }
 
+template <typename T>
+static void launch_backward(const muon_norm_grad_args& a, const Drop& d, float* parts, hipStream_t stream) {
+  const RowShape s = row_shape(a.cols);
+  const int64_t groups = (a.rows + s.per_group - 1) / s.per_group;
+  const dim3 grid((unsigned)(a.dweight ? norm_parts(a.rows, a.cols) : std::min(groups, resident(s.threads))));
+  const dim3 block(s.threads);
+  if (s.lpr == 8) MUON_LAUNCH("norm_bwd", (norm_bwd<T, 1, 8>), grid, block, stream, a, d, parts);
+  else if (s.lpr == 16) MUON_LAUNCH("norm_bwd", (norm_bwd<T, 1, 16>), grid, block, stream, a, d, parts);
+  else if (s.lpr == 32) MUON_LAUNCH("norm_bwd", (norm_bwd<T, 1, 32>), grid, block, stream, a, d, parts);
+  else if (s.lpr == 64 && s.nc == 1) MUON_LAUNCH("norm_bwd", (norm_bwd<T, 1, 64>), grid, block, stream, a, d, parts);
+  else if (s.lpr == 64) MUON_LAUNCH("norm_bwd", (norm_bwd<T, 2, 64>), grid, block, stream, a, d, parts);
+  else if (s.nc == 1) MUON_LAUNCH("norm_bwd", (norm_bwd<T, 1, 0>), grid, block, stream, a, d, parts);
+  else if (s.nc == 2) MUON_LAUNCH("norm_bwd", (norm_bwd<T, 2, 0>), grid, block, stream, a, d, parts);
+  else if (s.nc == 4) MUON_LAUNCH("norm_bwd", (norm_bwd<T, 4, 0>), grid, block, stream, a, d, parts);
+  else MUON_LAUNCH("norm_bwd_long", norm_bwd_long<T>, grid, block, stream, a, d, parts);
+}
+
 hipError_t run_norm_backward(const muon_norm_grad_args& a, const Drop& d, float* parts, hipStream_t stream) {
-  const dim3 grid((unsigned)std::min<int64_t>(a.rows, kMaxGrid));
-  if (a.dresidual || a.dx) {
-    if (a.dtype == MUON_BF16) MUON_LAUNCH("norm_bwd", norm_bwd<bf16_t>, grid, dim3(NT), stream, a, d);
-    else MUON_LAUNCH("norm_bwd", norm_bwd<float>, grid, dim3(NT), stream, a, d);
+  if (a.rows > 0) {
+    if (a.dtype == MUON_BF16) launch_backward<bf16_t>(a, d, parts, stream);
+    else launch_backward<float>(a, d, parts, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.dweight) {
-    const int64_t n = norm_parts(a.rows, a.cols);
-    const unsigned blocks = (unsigned)((a.cols + NT - 1) / NT);
-    if (n > 0) {
-      const dim3 g2(blocks, (unsigned)n);
-      if (a.dtype == MUON_BF16) MUON_LAUNCH("norm_dw_part", norm_dw_part<bf16_t>, g2, dim3(NT), stream, a, parts);
-      else MUON_LAUNCH("norm_dw_part", norm_dw_part<float>, g2, dim3(NT), stream, a, parts);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
-    MUON_LAUNCH("norm_dw_sum", norm_dw_sum, dim3(blocks), dim3(NT), stream, a.cols, n, parts, a.dweight);
-  }
+  const int64_t n = norm_parts(a.rows, a.cols);
+  if (a.dweight && n != 1)   // n = 0: zeros
+    MUON_LAUNCH("norm_dw_sum", norm_dw_sum, dim3((unsigned)((a.cols + DWC - 1) / DWC)), dim3(DWC * DWL), stream, a.cols, n,
+                parts, a.dweight);
   return hipGetLastError();
 }
 

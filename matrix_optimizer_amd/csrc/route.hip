@@ -3,6 +3,8 @@
 #include <algorithm>
 #include <float.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "rows.h"
 
@@ -11,9 +13,42 @@ namespace {
 
 constexpr int RT = 256;                 // threads of a workgroup: four waves, a row each
 constexpr int RW = RT / WAVE;
-constexpr int64_t kMaxGrid = 1 << 16;
-constexpr int EPL = MUON_ROUTE_MAX_EXPERTS / WAVE;   // experts a lane may hold
 constexpr double kOut = -HUGE_VAL;      // rank of an expert that may not be chosen
+constexpr int kNone = INT32_MIN;        // the same as an ordered key
+
+// A row's experts over LPT lanes, NC chunks of eight to a lane: expert
+// (i LPT + t) 8 + j is element 8 i + j of the t-th lane.  64 / LPT rows a wave.
+
+// Value of another lane of the same row; every lane of the wave is active.
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) { return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true); }
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) { return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(int, v))); }
+
+// f over the LPT lanes of a row, the result in each of them: two exchanges
+// within four lanes, then mirrored halves of 8 and 16 lanes, then across the
+// wave.  f is commutative, so that both sides of an exchange agree.
+template <int LPT, class V, class F>
+__device__ __forceinline__ V over_row(V v, F f) {
+  v = f(v, dpp<0xB1>(v));                              // lane ^ 1
+  v = f(v, dpp<0x4E>(v));                              // lane ^ 2
+  if constexpr (LPT >= 8) v = f(v, dpp<0x141>(v));     // lane 7 - l of eight
+  if constexpr (LPT >= 16) v = f(v, dpp<0x140>(v));    // lane 15 - l of sixteen
+  if constexpr (LPT >= 32) v = f(v, __shfl_xor(v, 16, WAVE));
+  if constexpr (LPT >= 64) v = f(v, __shfl_xor(v, 32, WAVE));
+  return v;
+}
+__device__ __forceinline__ float max_f(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float add_f(float a, float b) { return a + b; }
+__device__ __forceinline__ int max_i(int a, int b) { return a > b ? a : b; }
+__device__ __forceinline__ int min_i(int a, int b) { return a < b ? a : b; }
+
+// Floats (no NaN) in the order of integers, and back.
+__device__ __forceinline__ int key_of(float v) {
+  const int b = __builtin_bit_cast(int, v + 0.f);   // -0 and 0 are one value
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float of_key(int k) { return __builtin_bit_cast(float, k ^ ((k >> 31) & 0x7fffffff)); }
 
 __device__ __forceinline__ double wave_sum64(double v) {
 #pragma unroll
@@ -37,281 +72,596 @@ __device__ __forceinline__ void wave_best(double& v, int& i) {
   }
 }
 
-// log sigmoid(l), l finite.
-__device__ __forceinline__ double log_sigmoid(double l) { return fmin(l, 0.0) - log1p(exp(-fabs(l))); }
-
-// A wave a row; lane l holds experts l, l + 64, ...; every score in 64 bits.
+// One row by the whole wave with every score in 64 bits.  It runs seldom and
+// keeps its values (E ranks, then G group values) in shared memory, so that it
+// takes few of the kernel's registers.
 template <typename T>
-__global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_args a) {
-  extern __shared__ double lds_all[];   // with groups: E values and `groups` results a wave
-  const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
-  const int E = (int)a.num_experts, K = s.top_k, G = s.groups;
-  double* by_l = lds_all + (size_t)wave * (E + G);
-  double* of_l = by_l + E;
-  for (int64_t r = blockIdx.x * (int64_t)RW + wave; r < a.rows; r += (int64_t)gridDim.x * RW) {
-    int32_t* idx_r = a.experts + r * K;
-    float* w_r = a.weights + r * K;
-    if (a.token_mask && a.token_mask[r] == 0) {
-      if (lane < K) {
-        idx_r[lane] = -1;
-        w_r[lane] = 0.f;
+__device__ __forceinline__ void route_row_64(const muon_route_spec& s, const muon_route_args& a, int64_t r,
+                                             double* rank) {
+  const int lane = threadIdx.x & (WAVE - 1);
+  const int E = (int)a.num_experts, K = s.top_k, G = s.groups, n = E / G;
+  const bool soft = s.score == MUON_SCORE_SOFTMAX;
+  double* of_l = rank + E;
+  const T* row = static_cast<const T*>(a.logits) + r * a.logits_stride;
+  float top = -HUGE_VALF;
+#pragma unroll 1
+  for (int e = lane; e < E; e += WAVE) top = fmaxf(top, read_logit(ld_as_f32(row, e)));
+  top = wave_max(top);
+  double total = 1.0;
+  if (soft) {
+    total = 0.0;
+#pragma unroll 1
+    for (int e = lane; e < E; e += WAVE) {
+      const float l = read_logit(ld_as_f32(row, e));
+      if (l > -HUGE_VALF) total += exp((double)l - (double)top);
+    }
+    total = wave_sum64(total);
+  }
+  wave_sync();
+#pragma unroll 1
+  for (int e = lane; e < E; e += WAVE) {
+    const double l = (double)read_logit(ld_as_f32(row, e));
+    const double x = exp(soft ? l - (double)top : -l);
+    const double v = (soft ? x / total : 1.0 / (1.0 + x)) + (a.bias ? (double)a.bias[e] : 0.0);
+    rank[e] = l > kOut ? v : kOut;
+  }
+  wave_sync();
+  if (G > 1) {
+#pragma unroll 1
+    for (int g = lane; g < G; g += WAVE) {
+      double b1 = kOut, b2 = kOut;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        const double v = rank[g * n + j];
+        b2 = fmax(b2, fmin(b1, v));
+        b1 = fmax(b1, v);
       }
-      if (a.scores)
-        for (int e = lane; e < E; e += WAVE) a.scores[r * E + e] = 0.f;
-      continue;
+      of_l[g] = s.group_top == 2 && b2 > kOut ? b1 + b2 : b1;
     }
-    const T* row = static_cast<const T*>(a.logits) + r * a.logits_stride;
-    float l[EPL];
-    double rank[EPL];
-    float top = -HUGE_VALF;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + i * WAVE;
-      l[i] = e < E ? read_logit(ld_as_f32(row, e)) : -HUGE_VALF;
-      top = fmaxf(top, l[i]);
+    wave_sync();
+  }
+#pragma unroll 1
+  for (int e = lane; e < E; e += WAVE) {
+    if (G > 1) {   // a group stays if fewer than top_groups are before it
+      const int g = e / n;
+      const double mine = of_l[g];
+      int before = 0;
+#pragma unroll 1
+      for (int q = 0; q < G; ++q) before += of_l[q] > mine || (of_l[q] == mine && q < g);
+      if (before >= s.top_groups) rank[e] = kOut;
     }
-    top = wave_max(top);
-    double total = 1.0;
-    if (s.score == MUON_SCORE_SOFTMAX) {
-      total = 0.0;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (l[i] > -HUGE_VALF) total += exp((double)l[i] - (double)top);
-      total = wave_sum64(total);
-    }
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + i * WAVE;
-      rank[i] = kOut;
-      if (e >= E) continue;
-      double v = 0.0;
-      const bool open = l[i] > -HUGE_VALF;
-      if (open)
-        v = s.score == MUON_SCORE_SOFTMAX ? exp((double)l[i] - (double)top) / total : 1.0 / (1.0 + exp(-(double)l[i]));
-      if (a.scores) a.scores[r * E + e] = (float)v;
-      if (a.bias) v += (double)a.bias[e];
-      if (open) rank[i] = a.bias ? v : (double)l[i];
-      if (G > 1) by_l[e] = open ? v : kOut;
-    }
-    if (G > 1) {
-      const int n = E / G;
-      wave_sync();
-      for (int g = lane; g < G; g += WAVE) {
-        double b1 = kOut, b2 = kOut;
-        for (int j = 0; j < n; ++j) {
-          const double v = by_l[g * n + j];
-          b2 = fmax(b2, fmin(b1, v));
-          b1 = fmax(b1, v);
-        }
-        of_l[g] = s.group_top == 2 && b2 > kOut ? b1 + b2 : b1;
+    if (!a.bias && rank[e] > kOut) rank[e] = (double)read_logit(ld_as_f32(row, e));
+  }
+  wave_sync();
+  int chosen = -1;   // lane k: the k-th expert
+#pragma unroll 1
+  for (int k = 0; k < K; ++k) {
+    double v = kOut;
+    int at = INT32_MAX;
+#pragma unroll 1
+    for (int e = lane; e < E; e += WAVE)
+      if (rank[e] > v) {   // ascending experts: the first of equals stays
+        v = rank[e];
+        at = e;
       }
-      wave_sync();
-      // a group stays if fewer than top_groups are before it
+    wave_best(v, at);
+    if (!(v > kOut)) break;   // uniform: nothing is left
+    if (lane == k) chosen = at;
+    if (lane == 0) rank[at] = kOut;
+    wave_sync();
+  }
+  // weights from log s, lane k its own
+  double ls = kOut;
+  if (chosen >= 0) {
+    const double lc = (double)read_logit(ld_as_f32(row, chosen));
+    ls = soft ? lc - (double)top : fmin(lc, 0.0) - log1p(exp(-fabs(lc)));   // log sigmoid
+  }
+  double w = 0.0;
+  if (s.renormalise) {
+    double m = ls;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int e = lane + i * WAVE;
-        if (e >= E) continue;
-        const int g = e / n;
-        const double mine = of_l[g];
-        int before = 0;
-        for (int q = 0; q < G; ++q) before += of_l[q] > mine || (of_l[q] == mine && q < g);
-        if (before >= s.top_groups) rank[i] = kOut;
-      }
-      wave_sync();
-    }
-    int chosen = -1;   // lane k: the k-th expert
-    for (int k = 0; k < K; ++k) {
-      double v = kOut;
-      int at = INT32_MAX;
+    for (int o = 32; o >= 1; o >>= 1) m = fmax(m, __shfl_xor(m, o, WAVE));
+    const double e = chosen >= 0 ? exp(ls - m) : 0.0;
+    const double sum = wave_sum64(e);
+    if (chosen >= 0) w = e / sum;
+  } else if (chosen >= 0) {
+    w = exp(ls) / total;
+  }
+  if (lane < K) {
+    a.experts[r * K + lane] = chosen;
+    a.weights[r * K + lane] = (float)(w * (double)s.scale);
+  }
+}
+
+// A chosen expert's score: exp(l - top), the difference's rounding made good,
+// or sigmoid(l) without loss at either end.
+__device__ __forceinline__ float slot_score(float l, float top, bool soft) {
+  if (soft) {
+    const float d = l - top, back = d + top;
+    if (!(d > -150.f)) return 0.f;   // also where l - top overflows
+    const float lost = (l - back) + ((back - d) - top);   // l - top = d + lost, exactly
+    return expf(d) * (1.f + lost);
+  }
+  const float e = expf(-fabsf(l));
+  return (l < 0.f ? e : 1.f) / (1.f + e);
+}
+
+// 1 - sigmoid(l) without cancellation.
+__device__ __forceinline__ float one_less_sigmoid(float l) {
+  const float e = expf(-fabsf(l));
+  return (l > 0.f ? e : 1.f) / (1.f + e);
+}
+
+// Load of a row's logits, -inf from E on.
+template <typename T, int LPT, int NC>
+__device__ __forceinline__ void load_logits(const T* row, int E, int t, float* l) {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (rank[i] > v) {   // ascending experts: the first of equals stays
-          v = rank[i];
-          at = lane + i * WAVE;
-        }
-      wave_best(v, at);
-      if (!(v > kOut)) break;   // uniform: nothing is left
-      if (lane == k) chosen = at;
+  for (int i = 0; i < NC; ++i) {
+    const int c = (i * LPT + t) * 8;
+    load8(row, c, E, l + 8 * i);
 #pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (lane + i * WAVE == at) rank[i] = kOut;
-    }
-    // weights from log s, lane k its own
-    double ls = kOut;
-    if (chosen >= 0) {
-      const double lc = (double)read_logit(ld_as_f32(row, chosen));
-      ls = s.score == MUON_SCORE_SOFTMAX ? lc - (double)top : log_sigmoid(lc);
-    }
-    double w = 0.0;
-    if (s.renormalise) {
-      double m = ls;
-#pragma unroll
-      for (int o = 32; o >= 1; o >>= 1) m = fmax(m, __shfl_xor(m, o, WAVE));
-      const double e = chosen >= 0 ? exp(ls - m) : 0.0;
-      const double sum = wave_sum64(e);
-      if (chosen >= 0) w = e / sum;
-    } else if (chosen >= 0) {
-      w = exp(ls) / total;
-    }
-    if (lane < K) {
-      idx_r[lane] = chosen;
-      w_r[lane] = (float)(w * (double)s.scale);
+    for (int j = 0; j < 8; ++j) {
+      l[8 * i + j] = read_logit(l[8 * i + j]);
+      if (c + j >= E) l[8 * i + j] = -HUGE_VALF;
     }
   }
 }
 
-// A wave a row.  dlogits from the chosen experts' a_k, spread over the row
-// through shared memory, and the dense terms.
-template <typename T>
-__global__ __launch_bounds__(RT) void route_bwd(muon_route_spec s, muon_route_grad_args a) {
-  extern __shared__ float lds_f[];
-  const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
-  const int E = (int)a.num_experts, K = s.top_k;
-  float* mine = lds_f + (size_t)wave * E;
-  for (int64_t r = blockIdx.x * (int64_t)RW + wave; r < a.rows; r += (int64_t)gridDim.x * RW) {
-    T* out = static_cast<T*>(a.dlogits) + r * a.dlogits_stride;
-    const T* row = static_cast<const T*>(a.logits) + r * a.logits_stride;
-    const int at = lane < K ? a.experts[r * K + lane] : -1;
-    const bool on = at >= 0 && at < E;
-    const bool any = __ballot(on) != 0;
-    for (int e = lane; e < E; e += WAVE) mine[e] = 0.f;
-    wave_sync();
-    const float w = on ? a.weights[r * K + lane] : 0.f;
-    float v = on ? w * a.dweights[r * K + lane] : 0.f;
-    const float sum = wave_sum(v);
-    if (s.renormalise) v -= w / s.scale * sum;
-    if (on) mine[at] = v;
-    wave_sync();
-    const bool soft = s.score == MUON_SCORE_SOFTMAX;
-    const float rest = soft && !s.renormalise ? sum : 0.f;
-    float l[EPL], sc[EPL];
-    float top = -HUGE_VALF, total = 0.f, dot = 0.f;
+// The experts of a row and their weights.
+//
+// The choice is defined on scores in 64 bits; computing them so took 3/4 of
+// the first kernel's time (275 us for 32768 rows of 256 experts in groups).
+// Here scores are formed in fp32 with a known bound on their error, the
+// largest are taken one by one, and a row whose order that bound does not
+// decide is done again by route_row_64 (about one row in 300 there).  Logits
+// order themselves exactly: without bias and groups nothing is in doubt.
+template <typename T, int LPT, int NC>
+__global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_args a) {
+  extern __shared__ double lds_all[];   // E values and G results a wave in 64 bits, or of each row in 32
+  __shared__ int chosen_all[RT / LPT][MUON_ROUTE_MAX_TOP_K];
+  constexpr int V = 8 * NC, RPW = WAVE / LPT;
+  const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE, t = lane & (LPT - 1);
+  const int E = (int)a.num_experts, K = s.top_k, G = s.groups;
+  double* group_lds = lds_all + (size_t)wave * (E + G) * (RPW > 2 ? RPW / 2 : 1);
+  int* chosen = chosen_all[threadIdx.x / LPT];
+  const bool soft = s.score == MUON_SCORE_SOFTMAX;
+  const bool doubt = a.bias || G > 1;                  // the choice reads scores
+  const bool need_z = soft && (doubt || a.scores || !s.renormalise);
+  // one tile of rows a workgroup: in a loop over tiles the compiler keeps every
+  // address and bias across it, 100 registers more
+  const int64_t tile = blockIdx.y * (int64_t)gridDim.x + blockIdx.x;
+  if (tile * RW * RPW >= a.rows) return;
+  // every lane stays to the end: rows past the last repeat it and store nothing
+  const int64_t want = (tile * RW + wave) * RPW + lane / LPT;
+  const bool live = want < a.rows;
+  const int64_t r = live ? want : a.rows - 1;
+  const bool masked = a.token_mask && a.token_mask[r] == 0;
+  const T* row = static_cast<const T*>(a.logits) + r * a.logits_stride;
+  float l[V];
+  load_logits<T, LPT, NC>(row, E, t, l);
+  float top = l[0];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + i * WAVE;
-      l[i] = e < E ? read_logit(ld_as_f32(row, e)) : -HUGE_VALF;
-      top = fmaxf(top, l[i]);
+  for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
+  top = over_row<LPT>(top, max_f);
+  float z = 1.f;
+  int key[V];
+  // error of a difference of two scores: sigmoid by the fast exp 2^-21 each;
+  // softmax (exp, sum of at most 20 in a row, quotient) 2^-18.4 of the largest
+  float tol = 0x1p-20f;
+  if (doubt || a.scores || need_z) {
+    float v[V];
+    if (soft) {
+      z = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        v[i] = l[i] > -HUGE_VALF ? expf(l[i] - top) : 0.f;
+        z += v[i];
+      }
+      z = over_row<LPT>(z, add_f);
+      const float inv = z > 0.f ? 1.f / z : 0.f;
+      tol = 0x1p-17f * inv;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] *= inv;
+    } else if (a.scores) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = 1.f / (1.f + expf(-l[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = __builtin_amdgcn_rcpf(1.f + __expf(-l[i]));
     }
-    top = wave_max(top);
+    if (a.scores && live) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      sc[i] = 0.f;
-      if (l[i] > -HUGE_VALF) sc[i] = soft ? expf(l[i] - top) : 1.f / (1.f + expf(-l[i]));
-      total += sc[i];
+      for (int i = 0; i < NC; ++i) {
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = masked ? 0.f : v[8 * i + j];
+        const int c = (i * LPT + t) * 8;
+        if (c < E) store8(a.scores + r * E, c, E, o);
+      }
+    }
+    if (a.bias) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        float b[8];
+        load8(a.bias, (i * LPT + t) * 8, E, b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[8 * i + j] += b[j];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = l[i] > -HUGE_VALF ? key_of(v[i]) : kNone;
+  }
+  bool unsure = false;
+  if (G > 1) {
+    // group values by way of shared memory: a lane a group, over its experts
+    float* by_l = reinterpret_cast<float*>(group_lds) + (size_t)(lane / LPT) * (E + G);
+    float* of_l = by_l + E;
+    const int n = E / G;
+    wave_sync();
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = ((i / 8) * LPT + t) * 8 + i % 8;
+      if (e < E) by_l[e] = l[i] > -HUGE_VALF ? of_key(key[i]) : -HUGE_VALF;
+    }
+    wave_sync();
+    for (int g = t; g < G; g += LPT) {
+      float b1 = -HUGE_VALF, b2 = -HUGE_VALF;
+      for (int j = 0; j < n; ++j) {
+        const float v = by_l[g * n + j];
+        b2 = fmaxf(b2, fminf(b1, v));
+        b1 = fmaxf(b1, v);
+      }
+      of_l[g] = s.group_top == 2 && b2 > -HUGE_VALF ? b1 + b2 : b1;
+    }
+    wave_sync();
+    // a group is in if fewer than top_groups may be before it, out if as many surely are
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = ((i / 8) * LPT + t) * 8 + i % 8;
+      if (e >= E) continue;
+      const int g = e / n;
+      const float mine = of_l[g], far = 2.f * tol + 0x1p-20f * fabsf(mine);
+      int sure = 0, may = 0;
+      if (mine > -HUGE_VALF) {
+        for (int q = 0; q < G; ++q) {
+          sure += of_l[q] > mine + far;
+          may += q != g && of_l[q] >= mine - far;
+        }
+        unsure |= may >= s.top_groups && sure < s.top_groups;
+      }
+      if (sure >= s.top_groups) key[i] = kNone;
+      else if (!a.bias && l[i] > -HUGE_VALF) key[i] = key_of(l[i]);
+    }
+  } else if (!a.bias) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = l[i] > -HUGE_VALF ? key_of(l[i]) : kNone;
+  }
+  wave_sync();
+  // the largest, one after another; with a bias also those after the last
+  // that its value does not set apart
+  float last = 0.f;
+  int last_at = -1;
+  bool open = a.bias != nullptr && !masked;   // whether what follows the last may still matter
+  for (int k = 0; k < K || (k < E && __any(open)); ++k) {
+    int m = key[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) m = max_i(m, key[i]);
+    m = over_row<LPT>(m, max_i);
+    int slot = V;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i) slot = key[i] == m ? i : slot;
+    const int mine = slot < V ? ((slot / 8) * LPT + t) * 8 + slot % 8 : INT32_MAX;
+    const int at = over_row<LPT>(mine, min_i);
+    const bool found = m != kNone;
+    if (k < K && t == 0) chosen[k] = found && !masked ? at : -1;
+    if (a.bias) {
+      const float v = of_key(m);
+      if (!found) {
+        open = false;
+      } else if (open && k > 0 && last - v <= tol + 0x1p-22f * (fabsf(last) + fabsf(v))) {
+        // too close to tell, unless the two are one value: then the index decides
+        if (ld_as_f32(row, at) != ld_as_f32(row, last_at) || a.bias[at] != a.bias[last_at]) {
+          unsure = true;
+          open = false;
+        }
+      } else if (k >= K) {
+        open = false;
+      }
+      last = v;
+      last_at = found ? at : last_at;
+    }
+    const int gone = mine == at ? slot : V;
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = i == gone ? kNone : key[i];
+  }
+  wave_sync();
+  // weights: lanes t, t + LPT, ... of the row's slots
+  float sum = 0.f;
+  bool any = false;
+  for (int k = t; k < K; k += LPT) {
+    const int at = chosen[k];
+    if (at < 0) continue;
+    any = true;
+    sum += slot_score(read_logit(ld_as_f32(row, at)), top, soft);
+  }
+  sum = over_row<LPT>(sum, add_f);
+  if (s.renormalise && any && !(sum > 0x1p-100f)) unsure = true;   // every score underflows: by logarithms
+  const float by = s.renormalise ? sum : z;
+  if (live) {
+    for (int k = t; k < K; k += LPT) {
+      const int at = chosen[k];
+      a.experts[r * K + k] = at;
+      a.weights[r * K + k] = at < 0 ? 0.f : s.scale * (slot_score(read_logit(ld_as_f32(row, at)), top, soft) / by);
+    }
+  }
+  uint64_t again = __ballot(unsure && live && !masked);
+  wave_sync();
+  while (again) {   // a row's lanes may all have set their bits
+    const int which = __ffsll((unsigned long long)again) - 1;
+    again &= ~((LPT < WAVE ? (uint64_t(1) << (LPT & 63)) - 1 : ~uint64_t(0)) << (which / LPT * LPT));
+    route_row_64<T>(s, a, (tile * RW + wave) * RPW + which / LPT, group_lds);
+  }
+}
+
+// A wave's rows' gradients.  The chosen experts' a_k reach their columns by
+// way of shared memory; the logits are read only where a dense term needs them.
+template <typename T, int LPT, int NC>
+__global__ __launch_bounds__(RT) void route_bwd(muon_route_spec s, muon_route_grad_args a) {
+  constexpr int V = 8 * NC, RPW = WAVE / LPT;
+  __shared__ float spread[RT / LPT][LPT * V];
+  const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE, t = lane & (LPT - 1);
+  const int E = (int)a.num_experts, K = s.top_k;
+  float* mine = spread[threadIdx.x / LPT];
+  const bool soft = s.score == MUON_SCORE_SOFTMAX;
+  const bool dense = a.dscores || (soft && !s.renormalise);
+  const int64_t tile = blockIdx.y * (int64_t)gridDim.x + blockIdx.x;
+  if (tile * RW * RPW >= a.rows) return;
+  const int64_t want = (tile * RW + wave) * RPW + lane / LPT;
+  const bool live = want < a.rows;
+  const int64_t r = live ? want : a.rows - 1;
+  const T* row = static_cast<const T*>(a.logits) + r * a.logits_stride;
+  wave_sync();
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mine[(i * LPT + t) * 8 + j] = 0.f;
+  float part = 0.f;
+  int some = 0;
+  for (int k = t; k < K; k += LPT) {
+    const int at = a.experts[r * K + k];
+    if (at < 0 || at >= E) continue;
+    some = 1;
+    part += a.weights[r * K + k] * a.dweights[r * K + k];
+  }
+  const float sum = over_row<LPT>(part, add_f);
+  some = over_row<LPT>(some, max_i);
+  wave_sync();
+  for (int k = t; k < K; k += LPT) {
+    const int at = a.experts[r * K + k];
+    if (at < 0 || at >= E) continue;
+    const float w = a.weights[r * K + k];
+    float v = w * a.dweights[r * K + k];
+    if (s.renormalise) v -= w / s.scale * sum;
+    if (!soft) v *= one_less_sigmoid(read_logit(ld_as_f32(row, at)));
+    mine[at] = v;
+  }
+  wave_sync();
+  float d[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) d[i] = mine[((i / 8) * LPT + t) * 8 + i % 8];
+  if (dense) {
+    float l[V], ds[V];
+    load_logits<T, LPT, NC>(row, E, t, l);
+#pragma unroll
+    for (int i = 0; i < V; ++i) ds[i] = 0.f;
+    if (a.dscores) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) load8(a.dscores + r * E, (i * LPT + t) * 8, E, ds + 8 * i);
     }
     if (soft) {
-      total = wave_sum(total);
+      float top = l[0], z = 0.f, dot = 0.f;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) sc[i] = sc[i] / total;
-    }
-    if (soft && a.dscores) {
+      for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
+      top = over_row<LPT>(top, max_f);
+      float p[V];
 #pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (l[i] > -HUGE_VALF) dot += sc[i] * a.dscores[r * E + lane + i * WAVE];
-      dot = wave_sum(dot);
-    }
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + i * WAVE;
-      if (e >= E) continue;
-      float d = 0.f;
-      if (any && l[i] > -HUGE_VALF) {
-        const float ds = a.dscores ? a.dscores[r * E + e] : 0.f;
-        const float q = l[i] >= 0.f ? expf(-l[i]) * sc[i] : 1.f - sc[i];   // 1 - sigmoid without cancellation
-        d = soft ? mine[e] - rest * sc[i] + (a.dscores ? sc[i] * (ds - dot) : 0.f) : (mine[e] + ds * sc[i]) * q;
+      for (int i = 0; i < V; ++i) {
+        p[i] = l[i] > -HUGE_VALF ? expf(l[i] - top) : 0.f;
+        z += p[i];
       }
-      st_from_f32(out, e, d);
+      z = over_row<LPT>(z, add_f);
+      const float inv = z > 0.f ? 1.f / z : 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        p[i] *= inv;
+        if (l[i] > -HUGE_VALF) dot += p[i] * ds[i];
+      }
+      dot = over_row<LPT>(dot, add_f) + (s.renormalise ? 0.f : sum);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (l[i] > -HUGE_VALF) d[i] += p[i] * (ds[i] - dot);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (!(l[i] > -HUGE_VALF)) continue;
+        const float q = one_less_sigmoid(l[i]);
+        d[i] += ds[i] * (1.f - q) * q;
+      }
     }
-    wave_sync();
+  }
+  if (live) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = (i * LPT + t) * 8;
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = some ? d[8 * i + j] : 0.f;
+      if (c < E) store8(static_cast<T*>(a.dlogits) + r * a.dlogits_stride, c, E, o);
+    }
   }
 }
 
 // ---- order of the pairs ----------------------------------------------------
-// A stable counting sort over tiles of pairs.  order_count leaves each tile's
-// count of every expert (and of pairs without one); order_place sums the
-// tiles before its own, then ranks its pairs in ascending order: a wave takes
-// 64 consecutive pairs, and lanes of equal experts find each other by one
-// ballot for each bit of the expert's number.
-constexpr int OT = 512, OW = OT / WAVE;
-constexpr int64_t kTile = 8192;         // pairs of a tile
+// A stable counting sort.  The pairs are cut into at most kMaxTiles tiles;
+// order_count leaves each tile's count of every expert (and, as expert E, of
+// the pairs without one), then each workgroup of order_place adds up the tiles
+// before its own and places its pairs.  A wave takes 64 consecutive pairs at a
+// time: lanes of one expert find each other by a ballot for each bit of the
+// expert's number, and the lane's rank among them and the pairs of the wave
+// before is its place among the wave's.  One tile needs order_place alone.
+constexpr int OT = 1024, OW = OT / WAVE;
+constexpr int kChunks = 4;                           // of 64 pairs, a wave in a round
+constexpr int64_t kRound = OT * kChunks;             // pairs of a workgroup's round
+constexpr int64_t kMaxTiles = 256;                   // one to a CU
 
 __device__ __forceinline__ int read_expert(const int32_t* experts, int64_t p, int E) {
   const int e = experts[p];
   return e >= 0 && e < E ? e : E;
 }
 
-__global__ __launch_bounds__(OT) void order_count(int64_t pairs, int E, const int32_t* experts, int32_t* hist) {
+__global__ __launch_bounds__(OT) void order_count(int64_t pairs, int64_t tile, int E, const int32_t* experts,
+                                                  int32_t* hist) {
   extern __shared__ int32_t lds_i[];
   for (int e = threadIdx.x; e <= E; e += OT) lds_i[e] = 0;
   __syncthreads();
-  const int64_t from = blockIdx.x * kTile, to = from + kTile < pairs ? from + kTile : pairs;
+  const int64_t from = blockIdx.x * tile, to = from + tile < pairs ? from + tile : pairs;
+#pragma unroll 4
   for (int64_t p = from + threadIdx.x; p < to; p += OT) atomicAdd(&lds_i[read_expert(experts, p, E)], 1);
   __syncthreads();
   for (int e = threadIdx.x; e <= E; e += OT) hist[blockIdx.x * (int64_t)(E + 1) + e] = lds_i[e];
 }
 
-__global__ __launch_bounds__(OT) void order_place(int64_t pairs, int E, int64_t tiles, const int32_t* experts,
+// Shared memory of order_place, in 4-byte words: base, tot and sub of E + 1
+// each, two of OT + 1 for the partial sums, OW wave sums, and a 16-bit count a
+// wave and expert.
+__host__ __device__ constexpr int order_words(int E) {
+  return 3 * (E + 1) + 2 * (OT + 1) + OW + (OW * (E + 1) + 1) / 2;
+}
+
+__global__ __launch_bounds__(OT) void order_place(int64_t pairs, int64_t tile, int E, int tiles, const int32_t* experts,
                                                   const int32_t* hist, int32_t* counts, int32_t* offsets,
                                                   int32_t* order, int32_t* position) {
-  // next[w][e]: the place of wave w's next pair of expert e; tot[e]: all pairs of e
   extern __shared__ int32_t lds_i[];
-  int32_t* next = lds_i;
-  int32_t* tot = lds_i + (size_t)OW * (E + 1);
+  const int N = E + 1;
+  int32_t* base = lds_i;             // place of the round's first pair of each expert
+  int32_t* tot = base + N;           // all pairs of each expert
+  int32_t* sub = tot + N;            // the round's
+  int32_t* part = sub + N;           // [2][OT + 1]
+  int32_t* wsum = part + 2 * (OT + 1);
+  uint16_t* cnt = reinterpret_cast<uint16_t*>(wsum + OW);   // [OW][N]; at most kRound
   const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
-  constexpr int64_t per_wave = kTile / OW;
-  const int64_t from = blockIdx.x * kTile + wave * per_wave;
-  const int64_t to = from + per_wave < pairs ? from + per_wave : pairs;
-  for (int i = threadIdx.x; i < OW * (E + 1); i += OT) next[i] = 0;
-  __syncthreads();
-  for (int64_t p = from + lane; p < to; p += WAVE) atomicAdd(&next[wave * (E + 1) + read_expert(experts, p, E)], 1);
-  __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += OT) {
-    int before = 0, all = 0;
-    for (int64_t t = 0; t < tiles; ++t) {
-      const int n = hist[t * (E + 1) + e];
-      if (t < (int64_t)blockIdx.x) before += n;
-      all += n;
-    }
-    for (int w = 0; w < OW; ++w) {   // counts of the waves become places within the expert's group
-      const int n = next[w * (E + 1) + e];
-      next[w * (E + 1) + e] = before;
-      before += n;
-    }
-    tot[e] = all;
-  }
-  __syncthreads();
-  // exclusive sums over the experts, by one thread each (E + 1 is small)
-  for (int e = threadIdx.x; e <= E; e += OT) {
-    int before = 0;
-    for (int q = 0; q < e; ++q) before += tot[q];
-    for (int w = 0; w < OW; ++w) next[w * (E + 1) + e] += before;
-    if (blockIdx.x == 0) {
-      offsets[e] = before;
-      if (e < E) counts[e] = tot[e];
-    }
-  }
-  __syncthreads();
+  uint16_t* mine = cnt + (size_t)wave * N;
+  const int64_t from = blockIdx.x * tile, to = from + tile < pairs ? from + tile : pairs;
   int bits = 1;
   while ((1 << bits) <= E) ++bits;
-  for (int64_t p0 = from; p0 < to; p0 += WAVE) {
-    const int64_t p = p0 + lane;
-    const bool in = p < to;
-    const int e = in ? read_expert(experts, p, E) : 0;
-    uint64_t same = __ballot(in);
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t m = __ballot((e >> b) & 1);
-      same &= (e >> b) & 1 ? m : ~m;
+
+  if (tiles > 1) {
+    // pairs of each expert in the tiles before this one and in all: slices of
+    // the tiles side by side, as many as fit the workgroup
+    const int slices = OT / N > 0 ? OT / N : 1;
+    for (int i = threadIdx.x; i < slices * N; i += OT) {   // i < OT, or N = OT + 1
+      const int e = i % N, s0 = i / N;
+      int before = 0, all = 0;
+#pragma unroll 8
+      for (int t = s0; t < tiles; t += slices) {
+        const int n = hist[t * (int64_t)N + e];
+        all += n;
+        before += t < (int)blockIdx.x ? n : 0;
+      }
+      part[i] = before;
+      part[OT + 1 + i] = all;
     }
-    const int before = __popcll(same & ((uint64_t(1) << lane) - 1));
-    int place = 0;
-    if (in) place = next[wave * (E + 1) + e] + before;
-    wave_sync();
-    if (in && before == 0) next[wave * (E + 1) + e] += __popcll(same);
-    wave_sync();
-    if (in) {
-      order[place] = e < E ? (int32_t)p : -1;
-      position[p] = e < E ? place : -1;
+    __syncthreads();
+    for (int e = threadIdx.x; e < N; e += OT) {
+      int before = 0, all = 0;
+      for (int q = 0; q < slices; ++q) {
+        before += part[q * N + e];
+        all += part[OT + 1 + q * N + e];
+      }
+      base[e] = before;
+      tot[e] = all;
     }
+  }
+
+  for (int64_t p0 = from; p0 < to; p0 += kRound) {
+    for (int i = threadIdx.x; i < OW * N; i += OT) cnt[i] = 0;
+    int ex[kChunks], rank[kChunks];
+    const int64_t first = p0 + (int64_t)wave * (kChunks * WAVE) + lane;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) ex[c] = first + c * WAVE < to ? read_expert(experts, first + c * WAVE, E) : -1;
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      uint64_t same = __ballot(ex[c] >= 0);
+      for (int b = 0; b < bits; ++b) {
+        const bool bit = (ex[c] >> b) & 1;
+        const uint64_t m = __ballot(bit);
+        same &= bit ? m : ~m;
+      }
+      const int before = __popcll(same & ((uint64_t(1) << lane) - 1));
+      const int so_far = ex[c] >= 0 ? mine[ex[c]] : 0;
+      rank[c] = so_far + before;
+      wave_sync();
+      if (ex[c] >= 0 && before == 0) mine[ex[c]] = (uint16_t)(so_far + __popcll(same));
+      wave_sync();
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < N; e += OT) {   // counts of the waves become their first places
+      int run = 0;
+#pragma unroll
+      for (int w = 0; w < OW; ++w) {
+        const int n = cnt[w * N + e];
+        cnt[w * N + e] = (uint16_t)run;
+        run += n;
+      }
+      sub[e] = run;
+      if (tiles == 1) {
+        base[e] = 0;
+        tot[e] = run;
+      }
+    }
+    __syncthreads();
+    if (p0 == from) {
+      // the experts' first places: exclusive sums of the totals, E <= OT
+      const int v = (int)threadIdx.x < E ? tot[threadIdx.x] : 0;
+      int run = v;
+#pragma unroll
+      for (int o = 1; o < WAVE; o <<= 1) {
+        const int up = __shfl_up(run, o, WAVE);
+        run += lane >= o ? up : 0;
+      }
+      if (lane == WAVE - 1) wsum[wave] = run;
+      __syncthreads();
+      int before = 0, total = 0;
+#pragma unroll
+      for (int w = 0; w < OW; ++w) {
+        before += w < wave ? wsum[w] : 0;
+        total += wsum[w];
+      }
+      if ((int)threadIdx.x < E) {
+        base[threadIdx.x] += before + run - v;
+        if (blockIdx.x == 0) {
+          offsets[threadIdx.x] = before + run - v;
+          counts[threadIdx.x] = v;
+        }
+      }
+      if (threadIdx.x == 0) {
+        base[E] += total;
+        if (blockIdx.x == 0) offsets[E] = total;
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int e = ex[c];
+      if (e < 0) continue;
+      const int place = base[e] + (int)mine[e] + rank[c];
+      order[place] = e < E ? (int32_t)(first + c * WAVE) : -1;
+      position[first + c * WAVE] = e < E ? place : -1;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < N; e += OT) base[e] += sub[e];
+    __syncthreads();
   }
 }
 
@@ -341,38 +691,78 @@ __global__ __launch_bounds__(RT) void balance_k(int E, const int32_t* counts, co
 
 }  // namespace
 
+// A workgroup a tile, in two dimensions: the lanes of one are below 2^32.
+static dim3 tile_grid(int64_t tiles) {
+  const int64_t x = std::min<int64_t>(tiles, 1 << 20);
+  return dim3((unsigned)x, (unsigned)((tiles + x - 1) / x));
+}
+
+// Lanes of a row and chunks of a lane by the number of experts: 16 lanes of
+// one or two chunks for the common sizes.
+template <class F>
+static void by_experts(int64_t experts, F f) {
+  if (experts <= 32) f(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
+  else if (experts <= 64) f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
+  else if (experts <= 128) f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
+  else if (experts <= 256) f(std::integral_constant<int, 16>(), std::integral_constant<int, 2>());
+  else if (experts <= 512) f(std::integral_constant<int, 32>(), std::integral_constant<int, 2>());
+  else f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
+}
+
+template <typename T>
+static void launch_route_forward(const muon_route_spec& s, const muon_route_args& a, hipStream_t stream) {
+  by_experts(a.num_experts, [&](auto lpt, auto nc) {
+    constexpr int LPT = decltype(lpt)::value, NC = decltype(nc)::value, per = RW * (WAVE / LPT);
+    const dim3 grid = tile_grid((a.rows + per - 1) / per);
+    const size_t shm = size_t(RW) * size_t(a.num_experts + s.groups) * std::max(sizeof(double), sizeof(float) * (WAVE / LPT));
+    MUON_LAUNCH_SHM("route_fwd", (route_fwd<T, LPT, NC>), grid, dim3(RT), shm, stream, s, a);
+  });
+}
+
 hipError_t run_route_forward(const muon_route_spec& s, const muon_route_args& a, hipStream_t stream) {
-  const dim3 grid((unsigned)std::min<int64_t>((a.rows + RW - 1) / RW, kMaxGrid));
-  const size_t shm = s.groups > 1 ? size_t(RW) * size_t(a.num_experts + s.groups) * sizeof(double) : 0;
-  if (a.dtype == MUON_BF16) MUON_LAUNCH_SHM("route_fwd", route_fwd<bf16_t>, grid, dim3(RT), shm, stream, s, a);
-  else MUON_LAUNCH_SHM("route_fwd", route_fwd<float>, grid, dim3(RT), shm, stream, s, a);
+  if (a.dtype == MUON_BF16) launch_route_forward<bf16_t>(s, a, stream);
+  else launch_route_forward<float>(s, a, stream);
   return hipGetLastError();
+}
+
+template <typename T>
+static void launch_route_backward(const muon_route_spec& s, const muon_route_grad_args& a, hipStream_t stream) {
+  by_experts(a.num_experts, [&](auto lpt, auto nc) {
+    constexpr int LPT = decltype(lpt)::value, NC = decltype(nc)::value, per = RW * (WAVE / LPT);
+    const dim3 grid = tile_grid((a.rows + per - 1) / per);
+    MUON_LAUNCH("route_bwd", (route_bwd<T, LPT, NC>), grid, dim3(RT), stream, s, a);
+  });
 }
 
 hipError_t run_route_backward(const muon_route_spec& s, const muon_route_grad_args& a, hipStream_t stream) {
-  const dim3 grid((unsigned)std::min<int64_t>((a.rows + RW - 1) / RW, kMaxGrid));
-  const size_t shm = size_t(RW) * size_t(a.num_experts) * sizeof(float);
-  if (a.dtype == MUON_BF16) MUON_LAUNCH_SHM("route_bwd", route_bwd<bf16_t>, grid, dim3(RT), shm, stream, s, a);
-  else MUON_LAUNCH_SHM("route_bwd", route_bwd<float>, grid, dim3(RT), shm, stream, s, a);
+  if (a.dtype == MUON_BF16) launch_route_backward<bf16_t>(s, a, stream);
+  else launch_route_backward<float>(s, a, stream);
   return hipGetLastError();
 }
 
-int64_t order_tiles(int64_t pairs) { return (pairs + kTile - 1) / kTile; }
+// Pairs of a tile: whole rounds, as many as keep the tiles to one a CU.
+static int64_t order_tile(int64_t pairs) {
+  const int64_t rounds = (pairs + kRound - 1) / kRound;
+  return kRound * std::max<int64_t>(1, (rounds + kMaxTiles - 1) / kMaxTiles);
+}
+int64_t order_tiles(int64_t pairs) { return (pairs + order_tile(pairs) - 1) / order_tile(pairs); }
 
 hipError_t run_route_order(int64_t pairs, int64_t experts_n, const int32_t* experts, int32_t* counts, int32_t* offsets,
                            int32_t* order, int32_t* position, int32_t* ws, hipStream_t stream) {
   const int E = (int)experts_n;
-  const int64_t tiles = order_tiles(pairs);
+  const int64_t tile = order_tile(pairs), tiles = order_tiles(pairs);
   if (tiles == 0) {
     MUON_LAUNCH("order_none", order_none, dim3(1), dim3(OT), stream, E, counts, offsets);
     return hipGetLastError();
   }
-  MUON_LAUNCH_SHM("order_count", order_count, dim3((unsigned)tiles), dim3(OT), size_t(E + 1) * 4, stream, pairs, E,
-                  experts, ws);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  MUON_LAUNCH_SHM("order_place", order_place, dim3((unsigned)tiles), dim3(OT), size_t(OW + 1) * size_t(E + 1) * 4,
-                  stream, pairs, E, tiles, experts, ws, counts, offsets, order, position);
+  if (tiles > 1) {
+    MUON_LAUNCH_SHM("order_count", order_count, dim3((unsigned)tiles), dim3(OT), size_t(E + 1) * 4, stream, pairs, tile,
+                    E, experts, ws);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  MUON_LAUNCH_SHM("order_place", order_place, dim3((unsigned)tiles), dim3(OT), size_t(order_words(E)) * 4, stream, pairs,
+                  tile, E, (int)tiles, experts, ws, counts, offsets, order, position);
   return hipGetLastError();
 }
 

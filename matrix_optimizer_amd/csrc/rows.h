@@ -20,28 +20,53 @@ __device__ __forceinline__ void unpack8(const u32x4& v, float* f) {
   }
 }
 
-// Columns c .. c+7 of a row as fp32, zeros from column `cols` on.
-__device__ __forceinline__ void load8(const bf16_t* row, int64_t c, int64_t cols, float* f) {
-  if (c + 8 <= cols) {
-    const u32x4 v = *reinterpret_cast<const u32x4_any*>(row + c);
-    unpack8(v, f);
-  } else {
+// Columns c .. c+7 of a row in their stored form, zeros from column `cols` on
+// (c may lie past it): 4 registers of bf16 or 8 of fp32, so that loads can be
+// in flight while the row before is worked on.
+template <typename T> struct Chunk;
+template <> struct Chunk<bf16_t> {
+  u32x4 v;
+  __device__ __forceinline__ void load(const bf16_t* row, int64_t c, int64_t cols) {
+    if (c + 8 <= cols) {
+      v = *reinterpret_cast<const u32x4_any*>(row + c);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = c + j < cols ? bf2f(row[c + j]) : 0.f;
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t lo = c + 2 * q < cols ? row[c + 2 * q] : 0, hi = c + 2 * q + 1 < cols ? row[c + 2 * q + 1] : 0;
+        v[q] = lo | (hi << 16);
+      }
+    }
   }
-}
-__device__ __forceinline__ void load8(const float* row, int64_t c, int64_t cols, float* f) {
-  if (c + 8 <= cols) {
-    const u32x4 a = *reinterpret_cast<const u32x4_any*>(row + c), b = *reinterpret_cast<const u32x4_any*>(row + c + 4);
+  __device__ __forceinline__ void get(float* f) const { unpack8(v, f); }
+};
+template <> struct Chunk<float> {
+  u32x4 a, b;
+  __device__ __forceinline__ void load(const float* row, int64_t c, int64_t cols) {
+    if (c + 8 <= cols) {
+      a = *reinterpret_cast<const u32x4_any*>(row + c);
+      b = *reinterpret_cast<const u32x4_any*>(row + c + 4);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a[j] = c + j < cols ? __float_as_uint(row[c + j]) : 0;
+        b[j] = c + j + 4 < cols ? __float_as_uint(row[c + j + 4]) : 0;
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float* f) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       f[j] = __uint_as_float(a[j]);
       f[j + 4] = __uint_as_float(b[j]);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = c + j < cols ? row[c + j] : 0.f;
   }
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int64_t c, int64_t cols, float* f) {
+  Chunk<T> k;
+  k.load(row, c, cols);
+  k.get(f);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -154,31 +179,31 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
-// Sum / maximum over the workgroup's WAVES waves, in wave order; `lds` holds
-// WAVES floats and may be reused after the call.
-template <int WAVES>
-__device__ __forceinline__ float group_sum(float v, float* lds) {
-  v = wave_sum(v);
-  if constexpr (WAVES == 1) return v;
-  if ((threadIdx.x & (WAVE - 1)) == 0) lds[threadIdx.x / WAVE] = v;
+// Sum / maximum over a workgroup of up to 8 waves, in wave order.  `lds` holds
+// two sets of 8 floats, zero at first; `turn` alternates 0 and 1 from call to
+// call on the same set, so that one barrier a call is enough: a wave that
+// writes a set again has passed the barrier of the call in between, and with
+// it every wave its reads of that set.
+struct GroupRed {
+  float s[2][8];
+};
+__device__ __forceinline__ void red_init(GroupRed& g) {
+  if (threadIdx.x < 16) g.s[threadIdx.x >> 3][threadIdx.x & 7] = 0.f;
   __syncthreads();
-  float s = 0.f;
-#pragma unroll
-  for (int w = 0; w < WAVES; ++w) s += lds[w];
-  __syncthreads();
-  return s;
 }
-template <int WAVES>
-__device__ __forceinline__ float group_max(float v, float* lds) {
+__device__ __forceinline__ float group_sum(float v, GroupRed& g, int turn) {
+  v = wave_sum(v);
+  if ((threadIdx.x & (WAVE - 1)) == 0) g.s[turn][threadIdx.x / WAVE] = v;
+  __syncthreads();
+  const f32x4 a = *reinterpret_cast<const f32x4*>(g.s[turn]), b = *reinterpret_cast<const f32x4*>(g.s[turn] + 4);
+  return ((a[0] + a[1]) + (a[2] + a[3])) + ((b[0] + b[1]) + (b[2] + b[3]));
+}
+__device__ __forceinline__ float group_max(float v, GroupRed& g, int turn) {   // v >= 0
   v = wave_max(v);
-  if constexpr (WAVES == 1) return v;
-  if ((threadIdx.x & (WAVE - 1)) == 0) lds[threadIdx.x / WAVE] = v;
+  if ((threadIdx.x & (WAVE - 1)) == 0) g.s[turn][threadIdx.x / WAVE] = v;
   __syncthreads();
-  float s = lds[0];
-#pragma unroll
-  for (int w = 1; w < WAVES; ++w) s = fmaxf(s, lds[w]);
-  __syncthreads();
-  return s;
+  const f32x4 a = *reinterpret_cast<const f32x4*>(g.s[turn]), b = *reinterpret_cast<const f32x4*>(g.s[turn] + 4);
+  return fmaxf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), fmaxf(fmaxf(b[0], b[1]), fmaxf(b[2], b[3])));
 }
 
 }  // namespace muon

@@ -77,7 +77,7 @@ def test_route_sizes(e, k, score):
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("e,k,g,tg,gt", [(8, 2, 2, 1, 2), (8, 2, 8, 4, 2), (60, 4, 12, 3, 1), (64, 6, 8, 3, 2),
                                          (96, 4, 3, 2, 2), (256, 8, 8, 4, 2), (256, 8, 16, 1, 1), (1024, 8, 32, 5, 2),
-                                         (1000, 20, 100, 7, 2), (512, 3, 512, 3, 2), (21, 21, 7, 7, 2)])
+                                         (1000, 20, 100, 7, 2), (512, 3, 512, 3, 2), (1024, 8, 1024, 512, 2), (21, 21, 7, 7, 2)])
 @pytest.mark.parametrize("biased", [True, False])
 def test_route_groups(e, k, g, tg, gt, score, biased):
     rng = np.random.default_rng(e + g)
@@ -267,7 +267,7 @@ def check_order(experts, e):
 
 @pytest.mark.parametrize("e", [1, 2, 8, 60, 64, 255, 256, 1024])
 @pytest.mark.parametrize("n,k", [(1, 1), (7, 3), (16, 6), (64, 1), (1000, 8), (1023, 8), (1024, 8), (1025, 8),
-                                 (5000, 4), (40000, 6)])
+                                 (4096, 1), (4097, 1), (5000, 4), (40000, 6)])
 def test_order(n, k, e):
     rng = np.random.default_rng(n + e)
     idx = rng.integers(-1, e, (n, k)).astype(np.int32)
@@ -286,8 +286,10 @@ def test_order_lopsided():
         check_order(torch.empty(0, 4, dtype=torch.int32, device="cuda"), e)
 
 
-def test_order_large():
-    idx = torch.randint(-1, 256, (200000, 8), dtype=torch.int32, device="cuda",
+@pytest.mark.parametrize("n", [200000, 1100000])
+def test_order_large(n):
+    """More rounds than tiles: tiles of one and of several rounds."""
+    idx = torch.randint(-1, 256, (n, 8), dtype=torch.int32, device="cuda",
                         generator=torch.Generator(device="cuda").manual_seed(3))
     check_order(idx, 256)
 
