@@ -23,6 +23,8 @@ constexpr int kNone = INT32_MIN;        // the same as an ordered key
 template <int CTRL>
 __device__ __forceinline__ int dpp(int v) { return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true); }
 template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) { return (uint32_t)dpp<CTRL>((int)v); }
+template <int CTRL>
 __device__ __forceinline__ float dpp(float v) { return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(int, v))); }
 
 // f over the LPT lanes of a row, the result in each of them: two exchanges
@@ -42,6 +44,7 @@ __device__ __forceinline__ float max_f(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ float add_f(float a, float b) { return a + b; }
 __device__ __forceinline__ int max_i(int a, int b) { return a > b ? a : b; }
 __device__ __forceinline__ int min_i(int a, int b) { return a < b ? a : b; }
+__device__ __forceinline__ uint32_t min_u(uint32_t a, uint32_t b) { return a < b ? a : b; }
 
 // Floats (no NaN) in the order of integers, and back.
 __device__ __forceinline__ int key_of(float v) {
@@ -207,26 +210,55 @@ __device__ __forceinline__ void load_logits(const T* row, int E, int t, float* l
   }
 }
 
+// Shared memory of a row in the 32-bit choice (E values, then G group values
+// and G marks) and of a wave, which also fits route_row_64's.
+__host__ __device__ constexpr int route_wave_words(int E, int G, int rows) {
+  const int one = rows * (E + 2 * G), two = 2 * (E + G);
+  return ((one > two ? one : two) + 1) & ~1;
+}
+
+// Whether expert p, taken before q, is before it by the definition: s + b in
+// 64 bits, then the index.  A softmax's sum z is known in 32 bits; `known` is
+// false where that leaves the order open.
+__device__ __forceinline__ bool before_64(float lp, float lq, float bp, float bq, int p, int q, bool soft, float top,
+                                          float z, bool& known) {
+  const double ep = exp(soft ? (double)lp - (double)top : -(double)lp);
+  const double eq = exp(soft ? (double)lq - (double)top : -(double)lq);
+  const double sp = soft ? ep / (double)z : 1.0 / (1.0 + ep), sq = soft ? eq / (double)z : 1.0 / (1.0 + eq);
+  const double vp = sp + (double)bp, vq = sq + (double)bq;
+  known = !soft || fabs(vp - vq) > 0x1p-18 * fabs(sp - sq) || (lp == lq && bp == bq);
+  return vp > vq || (vp == vq && p < q);
+}
+
 // The experts of a row and their weights.
 //
-// The choice is defined on scores in 64 bits; computing them so took 3/4 of
-// the first kernel's time (275 us for 32768 rows of 256 experts in groups).
-// Here scores are formed in fp32 with a known bound on their error, the
-// largest are taken one by one, and a row whose order that bound does not
-// decide is done again by route_row_64 (about one row in 300 there).  Logits
-// order themselves exactly: without bias and groups nothing is in doubt.
+// The choice is defined on scores in 64 bits; forming and sorting them so took
+// 275 us for 32768 rows of 256 experts in groups, of which the bytes are 4.
+// What bounds it is the instructions of the choice, so a row gets 4 to 64
+// lanes (16 for 256 experts, four rows a wave), and the choice is made in
+// three grades, each for the rows that the one before leaves open:
+//   1. one 32-bit number holds the upper 22 bits of a value's ordered key and
+//      the expert, so that numbers differ and the next largest is the least of
+//      m - 1 - number as unsigned: 1.5 instructions an expert, nothing is
+//      marked.  bf16 logits fit whole; other values must differ in those bits
+//      (and scores by their error);
+//   2. the full 32-bit keys, the expert found and marked: 5.5 instructions;
+//      scores closer than their error are compared in 64 bits, two at a time;
+//   3. route_row_64.
+// Logits order themselves exactly: without bias and groups no score is needed
+// to choose.
 template <typename T, int LPT, int NC>
 __global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_args a) {
-  extern __shared__ double lds_all[];   // E values and G results a wave in 64 bits, or of each row in 32
+  extern __shared__ double lds_all[];
   __shared__ int chosen_all[RT / LPT][MUON_ROUTE_MAX_TOP_K];
   constexpr int V = 8 * NC, RPW = WAVE / LPT;
   const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE, t = lane & (LPT - 1);
   const int E = (int)a.num_experts, K = s.top_k, G = s.groups;
-  double* group_lds = lds_all + (size_t)wave * (E + G) * (RPW > 2 ? RPW / 2 : 1);
+  float* wave_lds = reinterpret_cast<float*>(lds_all) + (size_t)wave * route_wave_words(E, G, RPW);
   int* chosen = chosen_all[threadIdx.x / LPT];
   const bool soft = s.score == MUON_SCORE_SOFTMAX;
-  const bool doubt = a.bias || G > 1;                  // the choice reads scores
-  const bool need_z = soft && (doubt || a.scores || !s.renormalise);
+  const bool scored = a.bias || G > 1;                 // the choice reads scores
+  const bool need_z = soft && (scored || a.scores || !s.renormalise);
   // one tile of rows a workgroup: in a loop over tiles the compiler keeps every
   // address and bias across it, 100 registers more
   const int64_t tile = blockIdx.y * (int64_t)gridDim.x + blockIdx.x;
@@ -245,21 +277,27 @@ __global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_ar
   top = over_row<LPT>(top, max_f);
   float z = 1.f;
   int key[V];
-  // error of a difference of two scores: sigmoid by the fast exp 2^-21 each;
-  // softmax (exp, sum of at most 20 in a row, quotient) 2^-18.4 of the largest
-  float tol = 0x1p-20f;
-  if (doubt || a.scores || need_z) {
+  // Bound on the error of the difference of two scores.  Sigmoid: the fast exp
+  // is off by (2 |l| + 2) 2^-24, which enters with s (1 - s), the sum and the
+  // reciprocal by 3 2^-24: below 2^-22 each.  Softmax: (2 d + 2) 2^-24 e^-d for
+  // the exp, so at most 16 2^-24 of the sum (the mean d is at most log E), at
+  // most 20 roundings in a row in the sum, which two scores share, 3 after:
+  // below 2^-18 of the largest score for the difference.
+  float tol = 0x1p-21f;
+  if (scored || a.scores || need_z) {
     float v[V];
+    const bool fine = a.scores || !s.renormalise;   // results, not only the choice, come of these
     if (soft) {
       z = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        v[i] = l[i] > -HUGE_VALF ? expf(l[i] - top) : 0.f;
+        const float d = l[i] - top;
+        v[i] = !(l[i] > -HUGE_VALF) ? 0.f : fine ? expf(d) : __expf(d);
         z += v[i];
       }
       z = over_row<LPT>(z, add_f);
       const float inv = z > 0.f ? 1.f / z : 0.f;
-      tol = 0x1p-17f * inv;
+      tol = 0x1p-18f * inv;
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] *= inv;
     } else if (a.scores) {
@@ -291,88 +329,172 @@ __global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_ar
 #pragma unroll
     for (int i = 0; i < V; ++i) key[i] = l[i] > -HUGE_VALF ? key_of(v[i]) : kNone;
   }
-  bool unsure = false;
+  bool unsure = false;   // grade 3
+  uint32_t in = ~0u;     // bit i: element i's group stays
   if (G > 1) {
-    // group values by way of shared memory: a lane a group, over its experts
-    float* by_l = reinterpret_cast<float*>(group_lds) + (size_t)(lane / LPT) * (E + G);
+    float* by_l = wave_lds + (size_t)(lane / LPT) * (E + 2 * G);
     float* of_l = by_l + E;
-    const int n = E / G;
-    wave_sync();
+    int* in_l = reinterpret_cast<int*>(of_l + G);
+    const int n = E / G, span = n / 8;
+    // groups of 8 span experts, span a power of two up to a row's lanes: the
+    // same chunk of `span` neighbouring lanes, whose two best meet by exchange
+    const bool lanes = n % 8 == 0 && (span & (span - 1)) == 0 && span <= LPT;
+    if (lanes) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = ((i / 8) * LPT + t) * 8 + i % 8;
-      if (e < E) by_l[e] = l[i] > -HUGE_VALF ? of_key(key[i]) : -HUGE_VALF;
-    }
-    wave_sync();
-    for (int g = t; g < G; g += LPT) {
-      float b1 = -HUGE_VALF, b2 = -HUGE_VALF;
-      for (int j = 0; j < n; ++j) {
-        const float v = by_l[g * n + j];
-        b2 = fmaxf(b2, fminf(b1, v));
-        b1 = fmaxf(b1, v);
+      for (int i = 0; i < NC; ++i) {
+        float b1 = -HUGE_VALF, b2 = -HUGE_VALF;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float v = key[8 * i + j] == kNone ? -HUGE_VALF : of_key(key[8 * i + j]);
+          b2 = fmaxf(b2, fminf(b1, v));
+          b1 = fmaxf(b1, v);
+        }
+        auto meet = [&](float o1, float o2) {
+          b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+          b1 = fmaxf(b1, o1);
+        };
+        if (span > 1) meet(dpp<0xB1>(b1), dpp<0xB1>(b2));
+        if (span > 2) meet(dpp<0x4E>(b1), dpp<0x4E>(b2));
+        if (span > 4) meet(dpp<0x141>(b1), dpp<0x141>(b2));
+        if (span > 8) meet(dpp<0x140>(b1), dpp<0x140>(b2));
+        if (span > 16) meet(__shfl_xor(b1, 16, WAVE), __shfl_xor(b2, 16, WAVE));
+        if (span > 32) meet(__shfl_xor(b1, 32, WAVE), __shfl_xor(b2, 32, WAVE));
+        const int g = (i * LPT + t) / span;
+        if ((t & (span - 1)) == 0 && g < G) of_l[g] = s.group_top == 2 && b2 > -HUGE_VALF ? b1 + b2 : b1;
       }
-      of_l[g] = s.group_top == 2 && b2 > -HUGE_VALF ? b1 + b2 : b1;
+    } else {   // a lane a group, over its experts in shared memory
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = ((i / 8) * LPT + t) * 8 + i % 8;
+        if (e < E) by_l[e] = key[i] == kNone ? -HUGE_VALF : of_key(key[i]);
+      }
+      wave_sync();
+      for (int g = t; g < G; g += LPT) {
+        float b1 = -HUGE_VALF, b2 = -HUGE_VALF;
+        for (int j = 0; j < n; ++j) {
+          const float v = by_l[g * n + j];
+          b2 = fmaxf(b2, fminf(b1, v));
+          b1 = fmaxf(b1, v);
+        }
+        of_l[g] = s.group_top == 2 && b2 > -HUGE_VALF ? b1 + b2 : b1;
+      }
     }
     wave_sync();
-    // a group is in if fewer than top_groups may be before it, out if as many surely are
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = ((i / 8) * LPT + t) * 8 + i % 8;
-      if (e >= E) continue;
-      const int g = e / n;
-      const float mine = of_l[g], far = 2.f * tol + 0x1p-20f * fabsf(mine);
+    // a group is in if fewer than top_groups may be before it, out if as many
+    // surely are; one without an open expert is of no matter
+    for (int g = t; g < G; g += LPT) {
+      const float mine = of_l[g], far = 2.f * tol + 0x1p-21f * fabsf(mine);
       int sure = 0, may = 0;
       if (mine > -HUGE_VALF) {
         for (int q = 0; q < G; ++q) {
-          sure += of_l[q] > mine + far;
-          may += q != g && of_l[q] >= mine - far;
+          const float v = of_l[q];
+          sure += v > mine + far;
+          may += v >= mine - far;
         }
-        unsure |= may >= s.top_groups && sure < s.top_groups;
+        unsure |= may > s.top_groups && sure < s.top_groups;   // may counts the group itself
       }
-      if (sure >= s.top_groups) key[i] = kNone;
-      else if (!a.bias && l[i] > -HUGE_VALF) key[i] = key_of(l[i]);
+      in_l[g] = sure < s.top_groups;
     }
-  } else if (!a.bias) {
+    wave_sync();
+    if (lanes) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int g = (i * LPT + t) / span;
+        if (g < G && !in_l[g]) in &= ~(0xffu << (8 * i));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = ((i / 8) * LPT + t) * 8 + i % 8;
+        if (e < E && !in_l[e / n]) in &= ~(1u << i);
+      }
+    }
+  }
+  if (!a.bias) {
 #pragma unroll
     for (int i = 0; i < V; ++i) key[i] = l[i] > -HUGE_VALF ? key_of(l[i]) : kNone;
   }
-  wave_sync();
-  // the largest, one after another; with a bias also those after the last
-  // that its value does not set apart
-  float last = 0.f;
-  int last_at = -1;
-  bool open = a.bias != nullptr && !masked;   // whether what follows the last may still matter
-  for (int k = 0; k < K || (k < E && __any(open)); ++k) {
-    int m = key[0];
+  if (G > 1) {
 #pragma unroll
-    for (int i = 1; i < V; ++i) m = max_i(m, key[i]);
-    m = over_row<LPT>(m, max_i);
-    int slot = V;
+    for (int i = 0; i < V; ++i) key[i] = (in >> i) & 1 ? key[i] : kNone;
+  }
+
+  // grade 1
+  constexpr int kIndex = MUON_ROUTE_MAX_EXPERTS - 1;
+  const bool whole = !a.bias && sizeof(T) == 2;
+  bool open = false;     // grade 2
+  {
+    int num[V];
+    int m = kNone;
 #pragma unroll
-    for (int i = V - 1; i >= 0; --i) slot = key[i] == m ? i : slot;
-    const int mine = slot < V ? ((slot / 8) * LPT + t) * 8 + slot % 8 : INT32_MAX;
-    const int at = over_row<LPT>(mine, min_i);
-    const bool found = m != kNone;
-    if (k < K && t == 0) chosen[k] = found && !masked ? at : -1;
-    if (a.bias) {
-      const float v = of_key(m);
-      if (!found) {
-        open = false;
-      } else if (open && k > 0 && last - v <= tol + 0x1p-22f * (fabsf(last) + fabsf(v))) {
-        // too close to tell, unless the two are one value: then the index decides
-        if (ld_as_f32(row, at) != ld_as_f32(row, last_at) || a.bias[at] != a.bias[last_at]) {
-          unsure = true;
-          open = false;
-        }
-      } else if (k >= K) {
-        open = false;
-      }
-      last = v;
-      last_at = found ? at : last_at;
+    for (int i = 0; i < V; ++i) {
+      const int e = ((i / 8) * LPT + t) * 8 + i % 8;
+      num[i] = key[i] == kNone ? kNone : (key[i] & ~kIndex) | (kIndex - e);
+      m = max_i(m, num[i]);
     }
-    const int gone = mine == at ? slot : V;
+    m = over_row<LPT>(m, max_i);
+    int last = kNone;
+    for (int k = 0; k < K + !whole; ++k) {
+      const bool found = m != kNone;
+      if (k < K && t == 0) chosen[k] = found && !masked ? kIndex - (m & kIndex) : -1;
+      if (!whole && k > 0 && found) {
+        const float hi = of_key(last & ~kIndex), lo = of_key(m | kIndex);
+        open |= a.bias ? !(hi - lo > tol + 0x1p-23f * (fabsf(hi) + fabsf(lo))) : ((m ^ last) & ~kIndex) == 0;
+      }
+      last = m;
+      uint32_t d = ~0u;
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = i == gone ? kNone : key[i];
+      for (int i = 0; i < V; ++i) {
+        const uint32_t x = (uint32_t)m - 1u - (uint32_t)num[i];
+        d = x < d ? x : d;
+      }
+      d = over_row<LPT>(d, min_u);
+      m = found ? (int)((uint32_t)m - 1u - d) : kNone;
+    }
+    open = open && !masked && live;
+  }
+
+  // grade 2, for all rows of a wave that has one to do
+  if (__any(open)) {
+    float last = 0.f;
+    int last_at = 0;
+    bool more = a.bias != nullptr;   // whether what follows the last may still matter
+    for (int k = 0; k < K || (k < E && __any(more)); ++k) {
+      int m = key[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) m = max_i(m, key[i]);
+      m = over_row<LPT>(m, max_i);
+      int slot = V;
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i) slot = key[i] == m ? i : slot;
+      const int mine = slot < V ? ((slot / 8) * LPT + t) * 8 + slot % 8 : INT32_MAX;
+      const int at = over_row<LPT>(mine, min_i);
+      const bool found = m != kNone;
+      if (k < K && t == 0) chosen[k] = found && !masked ? at : -1;
+      if (a.bias) {
+        const float v = of_key(m);
+        if (!found) {
+          more = false;
+        } else if (more && k > 0) {
+          if (last - v > tol + 0x1p-23f * (fabsf(last) + fabsf(v))) {
+            more = k < K;
+          } else {
+            bool known;
+            const bool right = before_64(read_logit(ld_as_f32(row, last_at)), read_logit(ld_as_f32(row, at)),
+                                         a.bias[last_at], a.bias[at], last_at, at, soft, top, z, known);
+            if (!right || !known) {
+              unsure = true;
+              more = false;
+            }
+          }
+        }
+        last = v;
+        last_at = found ? at : last_at;
+      }
+      const int gone = mine == at ? slot : V;
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = i == gone ? kNone : key[i];
+    }
   }
   wave_sync();
   // weights: lanes t, t + LPT, ... of the row's slots
@@ -394,12 +516,13 @@ __global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_ar
       a.weights[r * K + k] = at < 0 ? 0.f : s.scale * (slot_score(read_logit(ld_as_f32(row, at)), top, soft) / by);
     }
   }
+  // grade 3
   uint64_t again = __ballot(unsure && live && !masked);
   wave_sync();
   while (again) {   // a row's lanes may all have set their bits
     const int which = __ffsll((unsigned long long)again) - 1;
     again &= ~((LPT < WAVE ? (uint64_t(1) << (LPT & 63)) - 1 : ~uint64_t(0)) << (which / LPT * LPT));
-    route_row_64<T>(s, a, (tile * RW + wave) * RPW + which / LPT, group_lds);
+    route_row_64<T>(s, a, (tile * RW + wave) * RPW + which / LPT, reinterpret_cast<double*>(wave_lds));
   }
 }
 
@@ -714,7 +837,7 @@ static void launch_route_forward(const muon_route_spec& s, const muon_route_args
   by_experts(a.num_experts, [&](auto lpt, auto nc) {
     constexpr int LPT = decltype(lpt)::value, NC = decltype(nc)::value, per = RW * (WAVE / LPT);
     const dim3 grid = tile_grid((a.rows + per - 1) / per);
-    const size_t shm = size_t(RW) * size_t(a.num_experts + s.groups) * std::max(sizeof(double), sizeof(float) * (WAVE / LPT));
+    const size_t shm = size_t(RW) * route_wave_words((int)a.num_experts, s.groups, WAVE / LPT) * 4;
     MUON_LAUNCH_SHM("route_fwd", (route_fwd<T, LPT, NC>), grid, dim3(RT), shm, stream, s, a);
   });
 }
