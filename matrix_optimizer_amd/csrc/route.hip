@@ -60,7 +60,8 @@ __device__ __forceinline__ double wave_sum64(double v) {
 }
 
 // Logit as the definition reads it: NaN closed, +inf the largest finite value.
-__device__ __forceinline__ float read_logit(float l) { return l != l ? -HUGE_VALF : fminf(l, FLT_MAX); }
+// fmaxf of a NaN and a number is the number.
+__device__ __forceinline__ float read_logit(float l) { return fminf(fmaxf(l, -HUGE_VALF), FLT_MAX); }
 
 // The largest (value, then lowest index) over the wave.
 __device__ __forceinline__ void wave_best(double& v, int& i) {
@@ -237,11 +238,10 @@ __device__ __forceinline__ bool before_64(float lp, float lq, float bp, float bq
 // What bounds it is the instructions of the choice, so a row gets 4 to 64
 // lanes (16 for 256 experts, four rows a wave), and the choice is made in
 // three grades, each for the rows that the one before leaves open:
-//   1. one 32-bit number holds the upper 22 bits of a value's ordered key and
-//      the expert, so that numbers differ and the next largest is the least of
-//      m - 1 - number as unsigned: 1.5 instructions an expert, nothing is
-//      marked.  bf16 logits fit whole; other values must differ in those bits
-//      (and scores by their error);
+//   1. one 32-bit number holds 22 bits of a value and the expert, so that
+//      numbers differ and the next largest is the least of m - 1 - number as
+//      unsigned: 2 instructions an expert, nothing is marked.  bf16 logits fit
+//      whole; other values must differ in those bits (scores by their error);
 //   2. the full 32-bit keys, the expert found and marked: 5.5 instructions;
 //      scores closer than their error are compared in 64 bits, two at a time;
 //   3. route_row_64.
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_ar
   for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
   top = over_row<LPT>(top, max_f);
   float z = 1.f;
-  int key[V];
+  float v[V];            // what is ranked; -inf: may not be chosen
   // Bound on the error of the difference of two scores.  Sigmoid: the fast exp
   // is off by (2 |l| + 2) 2^-24, which enters with s (1 - s), the sum and the
   // reciprocal by 3 2^-24: below 2^-22 each.  Softmax: (2 d + 2) 2^-24 e^-d for
@@ -285,7 +285,6 @@ __global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_ar
   // below 2^-18 of the largest score for the difference.
   float tol = 0x1p-21f;
   if (scored || a.scores || need_z) {
-    float v[V];
     const bool fine = a.scores || !s.renormalise;   // results, not only the choice, come of these
     if (soft) {
       z = 0.f;
@@ -327,7 +326,7 @@ __global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_ar
       }
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = l[i] > -HUGE_VALF ? key_of(v[i]) : kNone;
+    for (int i = 0; i < V; ++i) v[i] = l[i] > -HUGE_VALF ? v[i] : -HUGE_VALF;
   }
   bool unsure = false;   // grade 3
   uint32_t in = ~0u;     // bit i: element i's group stays
@@ -345,9 +344,8 @@ __global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_ar
         float b1 = -HUGE_VALF, b2 = -HUGE_VALF;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float v = key[8 * i + j] == kNone ? -HUGE_VALF : of_key(key[8 * i + j]);
-          b2 = fmaxf(b2, fminf(b1, v));
-          b1 = fmaxf(b1, v);
+          b2 = fmaxf(b2, fminf(b1, v[8 * i + j]));
+          b1 = fmaxf(b1, v[8 * i + j]);
         }
         auto meet = [&](float o1, float o2) {
           b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
@@ -366,15 +364,15 @@ __global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_ar
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int e = ((i / 8) * LPT + t) * 8 + i % 8;
-        if (e < E) by_l[e] = key[i] == kNone ? -HUGE_VALF : of_key(key[i]);
+        if (e < E) by_l[e] = v[i];
       }
       wave_sync();
       for (int g = t; g < G; g += LPT) {
         float b1 = -HUGE_VALF, b2 = -HUGE_VALF;
         for (int j = 0; j < n; ++j) {
-          const float v = by_l[g * n + j];
-          b2 = fmaxf(b2, fminf(b1, v));
-          b1 = fmaxf(b1, v);
+          const float x = by_l[g * n + j];
+          b2 = fmaxf(b2, fminf(b1, x));
+          b1 = fmaxf(b1, x);
         }
         of_l[g] = s.group_top == 2 && b2 > -HUGE_VALF ? b1 + b2 : b1;
       }
@@ -387,9 +385,9 @@ __global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_ar
       int sure = 0, may = 0;
       if (mine > -HUGE_VALF) {
         for (int q = 0; q < G; ++q) {
-          const float v = of_l[q];
-          sure += v > mine + far;
-          may += v >= mine - far;
+          const float x = of_l[q];
+          sure += x > mine + far;
+          may += x >= mine - far;
         }
         unsure |= may > s.top_groups && sure < s.top_groups;   // may counts the group itself
       }
@@ -412,42 +410,48 @@ __global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_ar
   }
   if (!a.bias) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = l[i] > -HUGE_VALF ? key_of(l[i]) : kNone;
+    for (int i = 0; i < V; ++i) v[i] = l[i];
   }
   if (G > 1) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = (in >> i) & 1 ? key[i] : kNone;
+    for (int i = 0; i < V; ++i) v[i] = (in >> i) & 1 ? v[i] : -HUGE_VALF;
   }
 
   // grade 1
-  constexpr int kIndex = MUON_ROUTE_MAX_EXPERTS - 1;
+  constexpr int kIndex = MUON_ROUTE_MAX_EXPERTS - 1, kLow = -(1 << 21);
   const bool whole = !a.bias && sizeof(T) == 2;
   bool open = false;     // grade 2
   {
     int num[V];
     int m = kNone;
+    // 22 bits of a value: a bf16 logit's ordered key, or steps below the
+    // largest, of 2^-20 in a range of 2 for scores and of 2^-17 in 32 for
+    // logits; values are in order where their steps differ, and scores where
+    // these differ by `apart`
+    float most = v[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) most = fmaxf(most, v[i]);
+    most = over_row<LPT>(most, max_f);
+    const float by = a.bias ? 0x1p20f : 0x1p17f;
+    const int apart = a.bias ? (int)fminf(2.f + 0x1p20f * (tol + 0x1p-22f * (fabsf(most) + 2.f)), 0x1p22f) : 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = ((i / 8) * LPT + t) * 8 + i % 8;
-      num[i] = key[i] == kNone ? kNone : (key[i] & ~kIndex) | (kIndex - e);
+      const int q = whole ? key_of(v[i]) >> 10 : (int)fmaxf((v[i] - most) * by, (float)kLow);
+      num[i] = v[i] > -HUGE_VALF ? q * (kIndex + 1) + (kIndex - e) : kNone;
       m = max_i(m, num[i]);
     }
     m = over_row<LPT>(m, max_i);
-    int last = kNone;
+    int last = 0;
     for (int k = 0; k < K + !whole; ++k) {
       const bool found = m != kNone;
       if (k < K && t == 0) chosen[k] = found && !masked ? kIndex - (m & kIndex) : -1;
-      if (!whole && k > 0 && found) {
-        const float hi = of_key(last & ~kIndex), lo = of_key(m | kIndex);
-        open |= a.bias ? !(hi - lo > tol + 0x1p-23f * (fabsf(hi) + fabsf(lo))) : ((m ^ last) & ~kIndex) == 0;
-      }
-      last = m;
+      const int q = m >> 10;
+      if (!whole && k > 0) open |= found && (last - q <= apart || q == kLow);
+      last = q;
       uint32_t d = ~0u;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const uint32_t x = (uint32_t)m - 1u - (uint32_t)num[i];
-        d = x < d ? x : d;
-      }
+      for (int i = 0; i < V; ++i) d = min_u(d, (uint32_t)m - 1u - (uint32_t)num[i]);
       d = over_row<LPT>(d, min_u);
       m = found ? (int)((uint32_t)m - 1u - d) : kNone;
     }
@@ -456,6 +460,9 @@ __global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_ar
 
   // grade 2, for all rows of a wave that has one to do
   if (__any(open)) {
+    int key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = v[i] > -HUGE_VALF ? key_of(v[i]) : kNone;
     float last = 0.f;
     int last_at = 0;
     bool more = a.bias != nullptr;   // whether what follows the last may still matter
@@ -472,11 +479,11 @@ __global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_ar
       const bool found = m != kNone;
       if (k < K && t == 0) chosen[k] = found && !masked ? at : -1;
       if (a.bias) {
-        const float v = of_key(m);
+        const float x = of_key(m);
         if (!found) {
           more = false;
         } else if (more && k > 0) {
-          if (last - v > tol + 0x1p-23f * (fabsf(last) + fabsf(v))) {
+          if (last - x > tol + 0x1p-23f * (fabsf(last) + fabsf(x))) {
             more = k < K;
           } else {
             bool known;
@@ -488,7 +495,7 @@ __global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_ar
             }
           }
         }
-        last = v;
+        last = x;
         last_at = found ? at : last_at;
       }
       const int gone = mine == at ? slot : V;
