@@ -25,6 +25,11 @@ __device__ __forceinline__ int dpp(int v) { return __builtin_amdgcn_mov_dpp(v, C
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) { return (uint32_t)dpp<CTRL>((int)v); }
 template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)(b >> 32)) << 32 | dpp<CTRL>((uint32_t)b));
+}
+template <int CTRL>
 __device__ __forceinline__ float dpp(float v) { return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(int, v))); }
 
 // f over the LPT lanes of a row, the result in each of them: two exchanges
@@ -43,15 +48,14 @@ __device__ __forceinline__ V over_row(V v, F f) {
 __device__ __forceinline__ float max_f(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ float add_f(float a, float b) { return a + b; }
 __device__ __forceinline__ int max_i(int a, int b) { return a > b ? a : b; }
-__device__ __forceinline__ int min_i(int a, int b) { return a < b ? a : b; }
+__device__ __forceinline__ double max_d(double a, double b) { return fmax(a, b); }
 __device__ __forceinline__ uint32_t min_u(uint32_t a, uint32_t b) { return a < b ? a : b; }
 
-// Floats (no NaN) in the order of integers, and back.
+// Floats (no NaN) in the order of integers.
 __device__ __forceinline__ int key_of(float v) {
   const int b = __builtin_bit_cast(int, v + 0.f);   // -0 and 0 are one value
   return b ^ ((b >> 31) & 0x7fffffff);
 }
-__device__ __forceinline__ float of_key(int k) { return __builtin_bit_cast(float, k ^ ((k >> 31) & 0x7fffffff)); }
 
 __device__ __forceinline__ double wave_sum64(double v) {
 #pragma unroll
@@ -63,22 +67,9 @@ __device__ __forceinline__ double wave_sum64(double v) {
 // fmaxf of a NaN and a number is the number.
 __device__ __forceinline__ float read_logit(float l) { return fminf(fmaxf(l, -HUGE_VALF), FLT_MAX); }
 
-// The largest (value, then lowest index) over the wave.
-__device__ __forceinline__ void wave_best(double& v, int& i) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
-    const double v2 = __shfl_xor(v, o, WAVE);
-    const int i2 = __shfl_xor(i, o, WAVE);
-    if (v2 > v || (v2 == v && i2 < i)) {
-      v = v2;
-      i = i2;
-    }
-  }
-}
-
-// One row by the whole wave with every score in 64 bits.  It runs seldom and
-// keeps its values (E ranks, then G group values) in shared memory, so that it
-// takes few of the kernel's registers.
+// One row by the whole wave with every score in 64 bits.  It runs seldom, and
+// then others wait for it: its values (E ranks, G group values, G marks) are
+// in shared memory, so that it takes few of the kernel's registers.
 template <typename T>
 __device__ __forceinline__ void route_row_64(const muon_route_spec& s, const muon_route_args& a, int64_t r,
                                              double* rank) {
@@ -86,13 +77,14 @@ __device__ __forceinline__ void route_row_64(const muon_route_spec& s, const muo
   const int E = (int)a.num_experts, K = s.top_k, G = s.groups, n = E / G;
   const bool soft = s.score == MUON_SCORE_SOFTMAX;
   double* of_l = rank + E;
+  double* in_l = of_l + G;
   const T* row = static_cast<const T*>(a.logits) + r * a.logits_stride;
   float top = -HUGE_VALF;
-#pragma unroll 1
-  for (int e = lane; e < E; e += WAVE) top = fmaxf(top, read_logit(ld_as_f32(row, e)));
-  top = wave_max(top);
   double total = 1.0;
   if (soft) {
+#pragma unroll 4
+    for (int e = lane; e < E; e += WAVE) top = fmaxf(top, read_logit(ld_as_f32(row, e)));
+    top = wave_max(top);
     total = 0.0;
 #pragma unroll 1
     for (int e = lane; e < E; e += WAVE) {
@@ -111,29 +103,42 @@ __device__ __forceinline__ void route_row_64(const muon_route_spec& s, const muo
   }
   wave_sync();
   if (G > 1) {
+    // the lanes shared out over the groups, each over its part of a group's experts
+    int share = WAVE;
+    while (share > 1 && share * G > WAVE) share >>= 1;
 #pragma unroll 1
-    for (int g = lane; g < G; g += WAVE) {
+    for (int g0 = 0; g0 < G; g0 += WAVE / share) {
+      const int g = g0 + lane / share;
       double b1 = kOut, b2 = kOut;
-#pragma unroll 1
-      for (int j = 0; j < n; ++j) {
-        const double v = rank[g * n + j];
-        b2 = fmax(b2, fmin(b1, v));
-        b1 = fmax(b1, v);
+      if (g < G) {
+#pragma unroll 4
+        for (int j = lane & (share - 1); j < n; j += share) {
+          const double v = rank[g * n + j];
+          b2 = fmax(b2, fmin(b1, v));
+          b1 = fmax(b1, v);
+        }
       }
-      of_l[g] = s.group_top == 2 && b2 > kOut ? b1 + b2 : b1;
+      for (int o = share >> 1; o >= 1; o >>= 1) {
+        const double o1 = __shfl_xor(b1, o, WAVE), o2 = __shfl_xor(b2, o, WAVE);
+        b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+        b1 = fmax(b1, o1);
+      }
+      if (g < G && (lane & (share - 1)) == 0) of_l[g] = s.group_top == 2 && b2 > kOut ? b1 + b2 : b1;
+    }
+    wave_sync();
+#pragma unroll 1
+    for (int g = lane; g < G; g += WAVE) {   // a group stays if fewer than top_groups are before it
+      const double mine = of_l[g];
+      int before = 0;
+#pragma unroll 4
+      for (int q = 0; q < G; ++q) before += of_l[q] > mine || (of_l[q] == mine && q < g);
+      in_l[g] = before < s.top_groups ? 1.0 : 0.0;
     }
     wave_sync();
   }
 #pragma unroll 1
   for (int e = lane; e < E; e += WAVE) {
-    if (G > 1) {   // a group stays if fewer than top_groups are before it
-      const int g = e / n;
-      const double mine = of_l[g];
-      int before = 0;
-#pragma unroll 1
-      for (int q = 0; q < G; ++q) before += of_l[q] > mine || (of_l[q] == mine && q < g);
-      if (before >= s.top_groups) rank[e] = kOut;
-    }
+    if (G > 1 && in_l[e / n] == 0.0) rank[e] = kOut;
     if (!a.bias && rank[e] > kOut) rank[e] = (double)read_logit(ld_as_f32(row, e));
   }
   wave_sync();
@@ -141,16 +146,20 @@ __device__ __forceinline__ void route_row_64(const muon_route_spec& s, const muo
 #pragma unroll 1
   for (int k = 0; k < K; ++k) {
     double v = kOut;
-    int at = INT32_MAX;
-#pragma unroll 1
-    for (int e = lane; e < E; e += WAVE)
-      if (rank[e] > v) {   // ascending experts: the first of equals stays
-        v = rank[e];
-        at = e;
-      }
-    wave_best(v, at);
+#pragma unroll 4
+    for (int e = lane; e < E; e += WAVE) v = fmax(v, rank[e]);
+    v = over_row<WAVE>(v, max_d);
     if (!(v > kOut)) break;   // uniform: nothing is left
+    int at = 0;               // the first expert of that rank: 64 at a time, in order
+    for (int e0 = 0; e0 < E; e0 += WAVE) {
+      const uint64_t m = __ballot(e0 + lane < E && rank[e0 + lane] == v);
+      if (m) {
+        at = e0 + __ffsll((unsigned long long)m) - 1;
+        break;
+      }
+    }
     if (lane == k) chosen = at;
+    wave_sync();
     if (lane == 0) rank[at] = kOut;
     wave_sync();
   }
@@ -162,9 +171,7 @@ __device__ __forceinline__ void route_row_64(const muon_route_spec& s, const muo
   }
   double w = 0.0;
   if (s.renormalise) {
-    double m = ls;
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) m = fmax(m, __shfl_xor(m, o, WAVE));
+    const double m = over_row<WAVE>(ls, max_d);
     const double e = chosen >= 0 ? exp(ls - m) : 0.0;
     const double sum = wave_sum64(e);
     if (chosen >= 0) w = e / sum;
@@ -175,6 +182,7 @@ __device__ __forceinline__ void route_row_64(const muon_route_spec& s, const muo
     a.experts[r * K + lane] = chosen;
     a.weights[r * K + lane] = (float)(w * (double)s.scale);
   }
+  wave_sync();
 }
 
 // A chosen expert's score: exp(l - top), the difference's rounding made good,
@@ -211,50 +219,46 @@ __device__ __forceinline__ void load_logits(const T* row, int E, int t, float* l
   }
 }
 
-// Shared memory of a row in the 32-bit choice (E values, then G group values
-// and G marks) and of a wave, which also fits route_row_64's.
-__host__ __device__ constexpr int route_wave_words(int E, int G, int rows) {
-  const int one = rows * (E + 2 * G), two = 2 * (E + G);
-  return ((one > two ? one : two) + 1) & ~1;
-}
+// Experts that the choice of a row may come down to: all of up to 32, else
+// the top_k (at most 32) and a few whose values are too near the last's.
+template <int LPT> struct Near {
+  static constexpr int CAP = LPT == 4 ? 32 : 40;
+};
 
-// Whether expert p, taken before q, is before it by the definition: s + b in
-// 64 bits, then the index.  A softmax's sum z is known in 32 bits; `known` is
-// false where that leaves the order open.
-__device__ __forceinline__ bool before_64(float lp, float lq, float bp, float bq, int p, int q, bool soft, float top,
-                                          float z, bool& known) {
-  const double ep = exp(soft ? (double)lp - (double)top : -(double)lp);
-  const double eq = exp(soft ? (double)lq - (double)top : -(double)lq);
-  const double sp = soft ? ep / (double)z : 1.0 / (1.0 + ep), sq = soft ? eq / (double)z : 1.0 / (1.0 + eq);
-  const double vp = sp + (double)bp, vq = sq + (double)bq;
-  known = !soft || fabs(vp - vq) > 0x1p-18 * fabs(sp - sq) || (lp == lq && bp == bq);
-  return vp > vq || (vp == vq && p < q);
+// Shared memory of a wave in 4-byte words: for `rows` rows side by side E
+// values, G group values and G marks, later `cap` times a 64-bit value, a
+// score and a place in the new order; or route_row_64's for one row.
+__host__ __device__ constexpr int route_wave_words(int E, int G, int rows, int cap) {
+  const int one = rows * (E + 2 * G), two = 2 * (E + 2 * G), three = rows * cap * 4;
+  const int most = one > two ? one : two;
+  return ((most > three ? most : three) + 1) & ~1;
 }
 
 // The experts of a row and their weights.
 //
 // The choice is defined on scores in 64 bits; forming and sorting them so took
 // 275 us for 32768 rows of 256 experts in groups, of which the bytes are 4.
-// What bounds it is the instructions of the choice, so a row gets 4 to 64
-// lanes (16 for 256 experts, four rows a wave), and the choice is made in
-// three grades, each for the rows that the one before leaves open:
+// What bounds it is the instructions of the choice, and at the end the longest
+// wave, so a row gets 4 to 64 lanes (16 for 256 experts, four rows a wave),
+// and the choice is made in three grades, each for the rows that the one
+// before leaves open:
 //   1. one 32-bit number holds 22 bits of a value and the expert, so that
 //      numbers differ and the next largest is the least of m - 1 - number as
 //      unsigned: 2 instructions an expert, nothing is marked.  bf16 logits fit
 //      whole; other values must differ in those bits (scores by their error);
-//   2. the full 32-bit keys, the expert found and marked: 5.5 instructions;
-//      scores closer than their error are compared in 64 bits, two at a time;
+//   2. the experts taken, and those after them that their bits do not set
+//      apart, in 64 bits, a lane each, and put in order by counting;
 //   3. route_row_64.
 // Logits order themselves exactly: without bias and groups no score is needed
 // to choose.
 template <typename T, int LPT, int NC>
-__global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_args a) {
+__global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route_args a) {
   extern __shared__ double lds_all[];
-  __shared__ int chosen_all[RT / LPT][MUON_ROUTE_MAX_TOP_K];
-  constexpr int V = 8 * NC, RPW = WAVE / LPT;
+  constexpr int V = 8 * NC, RPW = WAVE / LPT, CAP = Near<LPT>::CAP;
+  __shared__ int chosen_all[RT / LPT][CAP];
   const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE, t = lane & (LPT - 1);
   const int E = (int)a.num_experts, K = s.top_k, G = s.groups;
-  float* wave_lds = reinterpret_cast<float*>(lds_all) + (size_t)wave * route_wave_words(E, G, RPW);
+  float* wave_lds = reinterpret_cast<float*>(lds_all) + (size_t)wave * route_wave_words(E, G, RPW, CAP);
   int* chosen = chosen_all[threadIdx.x / LPT];
   const bool soft = s.score == MUON_SCORE_SOFTMAX;
   const bool scored = a.bias || G > 1;                 // the choice reads scores
@@ -421,6 +425,7 @@ __global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_ar
   constexpr int kIndex = MUON_ROUTE_MAX_EXPERTS - 1, kLow = -(1 << 21);
   const bool whole = !a.bias && sizeof(T) == 2;
   bool open = false;     // grade 2
+  int cands = 0;         // experts in `chosen`, more than K where the last's value is not apart
   {
     int num[V];
     int m = kNone;
@@ -442,66 +447,84 @@ __global__ __launch_bounds__(RT) void route_fwd(muon_route_spec s, muon_route_ar
       m = max_i(m, num[i]);
     }
     m = over_row<LPT>(m, max_i);
-    int last = 0;
-    for (int k = 0; k < K + !whole; ++k) {
-      const bool found = m != kNone;
-      if (k < K && t == 0) chosen[k] = found && !masked ? kIndex - (m & kIndex) : -1;
-      const int q = m >> 10;
-      if (!whole && k > 0) open |= found && (last - q <= apart || q == kLow);
-      last = q;
+    auto next = [&](int m) {   // the largest number below m; no number stays none
       uint32_t d = ~0u;
 #pragma unroll
       for (int i = 0; i < V; ++i) d = min_u(d, (uint32_t)m - 1u - (uint32_t)num[i]);
       d = over_row<LPT>(d, min_u);
-      m = found ? (int)((uint32_t)m - 1u - d) : kNone;
+      return m == kNone ? kNone : (int)((uint32_t)m - 1u - d);
+    };
+    int last = m;
+    for (int k = 0; k < K; ++k) {
+      if (t == 0) chosen[k] = m;
+      last = m;
+      m = next(m);
     }
-    open = open && !masked && live;
+    cands = K;
+    if (!whole) {
+      wave_sync();
+      for (int k = t; k < K; k += LPT)
+        open |= k > 0 && chosen[k] != kNone && (chosen[k - 1] >> 10) - (chosen[k] >> 10) <= apart;
+      // experts after the last, as long as they are not apart from it
+      bool more = !masked && last != kNone;
+      for (int k = K;; ++k) {
+        more = more && m != kNone && (last >> 10) - (m >> 10) <= apart;
+        if (more && k >= CAP) {
+          unsure = true;
+          more = false;
+        }
+        if (!__any(more)) break;
+        if (more) {
+          if (t == 0) chosen[k] = m;
+          cands = k + 1;
+          open = true;
+        }
+        m = next(m);
+      }
+      open = open && !masked && live;
+    }
   }
+  wave_sync();
+  for (int k = t; k < cands; k += LPT) {   // numbers become experts
+    const int m = chosen[k];
+    chosen[k] = m == kNone || masked ? -1 : kIndex - (m & kIndex);
+  }
+  wave_sync();
 
   // grade 2, for all rows of a wave that has one to do
   if (__any(open)) {
-    int key[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = v[i] > -HUGE_VALF ? key_of(v[i]) : kNone;
-    float last = 0.f;
-    int last_at = 0;
-    bool more = a.bias != nullptr;   // whether what follows the last may still matter
-    for (int k = 0; k < K || (k < E && __any(more)); ++k) {
-      int m = key[0];
-#pragma unroll
-      for (int i = 1; i < V; ++i) m = max_i(m, key[i]);
-      m = over_row<LPT>(m, max_i);
-      int slot = V;
-#pragma unroll
-      for (int i = V - 1; i >= 0; --i) slot = key[i] == m ? i : slot;
-      const int mine = slot < V ? ((slot / 8) * LPT + t) * 8 + slot % 8 : INT32_MAX;
-      const int at = over_row<LPT>(mine, min_i);
-      const bool found = m != kNone;
-      if (k < K && t == 0) chosen[k] = found && !masked ? at : -1;
+    double* val = reinterpret_cast<double*>(wave_lds) + (size_t)(lane / LPT) * CAP;
+    float* score = wave_lds + (size_t)RPW * CAP * 2 + (size_t)(lane / LPT) * CAP;
+    int* fresh = reinterpret_cast<int*>(score) + (size_t)RPW * CAP;
+    wave_sync();
+    int n = 0;   // the experts that there are
+    while (n < cands && chosen[n] >= 0) ++n;
+    for (int c = t; c < n; c += LPT) {
+      const float lc = read_logit(ld_as_f32(row, chosen[c]));
+      double x = (double)lc;
       if (a.bias) {
-        const float x = of_key(m);
-        if (!found) {
-          more = false;
-        } else if (more && k > 0) {
-          if (last - x > tol + 0x1p-23f * (fabsf(last) + fabsf(x))) {
-            more = k < K;
-          } else {
-            bool known;
-            const bool right = before_64(read_logit(ld_as_f32(row, last_at)), read_logit(ld_as_f32(row, at)),
-                                         a.bias[last_at], a.bias[at], last_at, at, soft, top, z, known);
-            if (!right || !known) {
-              unsure = true;
-              more = false;
-            }
-          }
-        }
-        last = x;
-        last_at = found ? at : last_at;
+        x = exp(soft ? x - (double)top : -x);
+        x = soft ? x / (double)z : 1.0 / (1.0 + x);
+        score[c] = (float)x;
+        x += (double)a.bias[chosen[c]];
       }
-      const int gone = mine == at ? slot : V;
-#pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = i == gone ? kNone : key[i];
+      val[c] = x;
     }
+    wave_sync();
+    for (int c = t; c < n; c += LPT) {
+      const double x = val[c];
+      const int e = chosen[c];
+      int before = 0;
+      for (int q = 0; q < n; ++q) {
+        const double y = val[q];
+        before += y > x || (y == x && chosen[q] < e);
+        // a softmax's sum is known in 32 bits: two values that it could turn round
+        if (a.bias && soft) unsure |= y != x && fabs(y - x) <= 0x1p-18 * (double)fabsf(score[q] - score[c]);
+      }
+      fresh[before] = e;
+    }
+    wave_sync();
+    for (int k = t; k < min(n, K); k += LPT) chosen[k] = fresh[k];
   }
   wave_sync();
   // weights: lanes t, t + LPT, ... of the row's slots
@@ -844,7 +867,7 @@ static void launch_route_forward(const muon_route_spec& s, const muon_route_args
   by_experts(a.num_experts, [&](auto lpt, auto nc) {
     constexpr int LPT = decltype(lpt)::value, NC = decltype(nc)::value, per = RW * (WAVE / LPT);
     const dim3 grid = tile_grid((a.rows + per - 1) / per);
-    const size_t shm = size_t(RW) * route_wave_words((int)a.num_experts, s.groups, WAVE / LPT) * 4;
+    const size_t shm = size_t(RW) * route_wave_words((int)a.num_experts, s.groups, WAVE / LPT, Near<LPT>::CAP) * 4;
     MUON_LAUNCH_SHM("route_fwd", (route_fwd<T, LPT, NC>), grid, dim3(RT), shm, stream, s, a);
   });
 }
