@@ -48,6 +48,7 @@ __device__ __forceinline__ V over_row(V v, F f) {
 __device__ __forceinline__ float max_f(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ float add_f(float a, float b) { return a + b; }
 __device__ __forceinline__ int max_i(int a, int b) { return a > b ? a : b; }
+__device__ __forceinline__ double add_d(double a, double b) { return a + b; }
 __device__ __forceinline__ double max_d(double a, double b) { return fmax(a, b); }
 __device__ __forceinline__ uint32_t min_u(uint32_t a, uint32_t b) { return a < b ? a : b; }
 
@@ -229,7 +230,7 @@ template <int LPT> struct Near {
 // values, G group values and G marks, later `cap` times a 64-bit value, a
 // score and a place in the new order; or route_row_64's for one row.
 __host__ __device__ constexpr int route_wave_words(int E, int G, int rows, int cap) {
-  const int one = rows * (E + 2 * G), two = 2 * (E + 2 * G), three = rows * cap * 4;
+  const int one = rows * (E + 2 * G), two = 2 * (E + 2 * G), three = rows * cap * 3;
   const int most = one > two ? one : two;
   return ((most > three ? most : three) + 1) & ~1;
 }
@@ -494,8 +495,16 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
   // grade 2, for all rows of a wave that has one to do
   if (__any(open)) {
     double* val = reinterpret_cast<double*>(wave_lds) + (size_t)(lane / LPT) * CAP;
-    float* score = wave_lds + (size_t)RPW * CAP * 2 + (size_t)(lane / LPT) * CAP;
-    int* fresh = reinterpret_cast<int*>(score) + (size_t)RPW * CAP;
+    int* fresh = reinterpret_cast<int*>(wave_lds + (size_t)RPW * CAP * 2) + (size_t)(lane / LPT) * CAP;
+    double total = 0.0;
+    if (a.bias && soft) {
+#pragma unroll 1
+      for (int i = 0; i < V; ++i) {
+        const int e = ((i / 8) * LPT + t) * 8 + i % 8;
+        if (e < E) total += exp((double)read_logit(ld_as_f32(row, e)) - (double)top);
+      }
+      total = over_row<LPT>(total, add_d);
+    }
     wave_sync();
     int n = 0;   // the experts that there are
     while (n < cands && chosen[n] >= 0) ++n;
@@ -504,8 +513,7 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
       double x = (double)lc;
       if (a.bias) {
         x = exp(soft ? x - (double)top : -x);
-        x = soft ? x / (double)z : 1.0 / (1.0 + x);
-        score[c] = (float)x;
+        x = soft ? x / total : 1.0 / (1.0 + x);
         x += (double)a.bias[chosen[c]];
       }
       val[c] = x;
@@ -518,8 +526,6 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
       for (int q = 0; q < n; ++q) {
         const double y = val[q];
         before += y > x || (y == x && chosen[q] < e);
-        // a softmax's sum is known in 32 bits: two values that it could turn round
-        if (a.bias && soft) unsure |= y != x && fabs(y - x) <= 0x1p-18 * (double)fabsf(score[q] - score[c]);
       }
       fresh[before] = e;
     }
@@ -527,24 +533,30 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
     for (int k = t; k < min(n, K); k += LPT) chosen[k] = fresh[k];
   }
   wave_sync();
-  // weights: lanes t, t + LPT, ... of the row's slots
-  float sum = 0.f;
+  // weights: lane t the row's slots t, t + LPT, ...
+  constexpr int SLOTS = (MUON_ROUTE_MAX_TOP_K + LPT - 1) / LPT;
+  int at[SLOTS];
+  float p[SLOTS], sum = 0.f;
   bool any = false;
-  for (int k = t; k < K; k += LPT) {
-    const int at = chosen[k];
-    if (at < 0) continue;
+#pragma unroll
+  for (int j = 0; j < SLOTS; ++j) {
+    const int k = t + j * LPT;
+    at[j] = k < K ? chosen[k] : -1;
+    p[j] = 0.f;
+    if (at[j] < 0) continue;
     any = true;
-    sum += slot_score(read_logit(ld_as_f32(row, at)), top, soft);
+    p[j] = slot_score(read_logit(ld_as_f32(row, at[j])), top, soft);
+    sum += p[j];
   }
   sum = over_row<LPT>(sum, add_f);
   if (s.renormalise && any && !(sum > 0x1p-100f)) unsure = true;   // every score underflows: by logarithms
   const float by = s.renormalise ? sum : z;
-  if (live) {
-    for (int k = t; k < K; k += LPT) {
-      const int at = chosen[k];
-      a.experts[r * K + k] = at;
-      a.weights[r * K + k] = at < 0 ? 0.f : s.scale * (slot_score(read_logit(ld_as_f32(row, at)), top, soft) / by);
-    }
+#pragma unroll
+  for (int j = 0; j < SLOTS; ++j) {
+    const int k = t + j * LPT;
+    if (!live || k >= K) continue;
+    a.experts[r * K + k] = at[j];
+    a.weights[r * K + k] = at[j] < 0 ? 0.f : s.scale * (p[j] / by);
   }
   // grade 3
   uint64_t again = __ballot(unsure && live && !masked);
