@@ -27,7 +27,7 @@ int64_t norm_parts(int64_t rows, int64_t cols);
 
 hipError_t run_route_forward(const muon_route_spec& s, const muon_route_args& a, hipStream_t stream);
 hipError_t run_route_backward(const muon_route_spec& s, const muon_route_grad_args& a, hipStream_t stream);
-// Tiles of pairs (each with num_experts + 1 counts in the workspace).
+// Tiles of pairs (each with num_experts + 1 counts in the workspace, in whole 16-byte pieces).
 int64_t order_tiles(int64_t pairs);
 hipError_t run_route_order(int64_t pairs, int64_t experts_n, const int32_t* experts, int32_t* counts, int32_t* offsets,
                            int32_t* order, int32_t* position, int32_t* ws, hipStream_t stream);

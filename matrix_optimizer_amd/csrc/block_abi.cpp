@@ -110,7 +110,7 @@ muon_status take_drop(const muon_dropout_spec* s, Drop& d) {
 muon_status hip_status(hipError_t e) { return e == hipSuccess ? MUON_OK : MUON_ERR_HIP; }
 hipStream_t hip_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 size_t order_bytes(int64_t pairs, int64_t experts) {
-  return align256(size_t(order_tiles(pairs)) * size_t(experts + 1) * 4);
+  return align256(size_t(order_tiles(pairs)) * size_t((experts + 4) & ~int64_t(3)) * 4);
 }
 
 muon_status check_route(const muon_route_spec* s, int64_t rows, int64_t experts, int dtype) {

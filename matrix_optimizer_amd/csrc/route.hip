@@ -679,6 +679,9 @@ constexpr int kChunks = 4;                           // of 64 pairs, a wave in a
 constexpr int64_t kRound = OT * kChunks;             // pairs of a workgroup's round
 constexpr int64_t kMaxTiles = 256;                   // one to a CU
 
+// Words of a tile's counts: E + 1, in whole 16-byte pieces.
+__host__ __device__ constexpr int order_pitch(int E) { return (E + 4) & ~3; }
+
 __device__ __forceinline__ int read_expert(const int32_t* experts, int64_t p, int E) {
   const int e = experts[p];
   return e >= 0 && e < E ? e : E;
@@ -687,20 +690,23 @@ __device__ __forceinline__ int read_expert(const int32_t* experts, int64_t p, in
 __global__ __launch_bounds__(OT) void order_count(int64_t pairs, int64_t tile, int E, const int32_t* experts,
                                                   int32_t* hist) {
   extern __shared__ int32_t lds_i[];
-  for (int e = threadIdx.x; e <= E; e += OT) lds_i[e] = 0;
+  const int pitch = order_pitch(E);
+  for (int e = threadIdx.x; e < pitch; e += OT) lds_i[e] = 0;
   __syncthreads();
   const int64_t from = blockIdx.x * tile, to = from + tile < pairs ? from + tile : pairs;
 #pragma unroll 4
   for (int64_t p = from + threadIdx.x; p < to; p += OT) atomicAdd(&lds_i[read_expert(experts, p, E)], 1);
   __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += OT) hist[blockIdx.x * (int64_t)(E + 1) + e] = lds_i[e];
+  for (int e = threadIdx.x; e < pitch; e += OT) hist[blockIdx.x * (int64_t)pitch + e] = lds_i[e];
 }
 
 // Shared memory of order_place, in 4-byte words: base, tot and sub of E + 1
-// each, two of OT + 1 for the partial sums, OW wave sums, and a 16-bit count a
-// wave and expert.
+// each, OW wave sums, and, one after the other, the partial sums over the
+// tiles (a 16-byte piece of two kinds a lane) and a 16-bit count a wave and
+// expert.
 __host__ __device__ constexpr int order_words(int E) {
-  return 3 * (E + 1) + 2 * (OT + 1) + OW + (OW * (E + 1) + 1) / 2;
+  const int sums = 2 * 4 * OT, cnt = (OW * (E + 1) + 1) / 2;
+  return 3 * order_pitch(E) + OW + (sums > cnt ? sums : cnt);
 }
 
 __global__ __launch_bounds__(OT) void order_place(int64_t pairs, int64_t tile, int E, int tiles, const int32_t* experts,
@@ -708,12 +714,13 @@ __global__ __launch_bounds__(OT) void order_place(int64_t pairs, int64_t tile, i
                                                   int32_t* order, int32_t* position) {
   extern __shared__ int32_t lds_i[];
   const int N = E + 1;
+  const int pitch = order_pitch(E);
   int32_t* base = lds_i;             // place of the round's first pair of each expert
-  int32_t* tot = base + N;           // all pairs of each expert
-  int32_t* sub = tot + N;            // the round's
-  int32_t* part = sub + N;           // [2][OT + 1]
-  int32_t* wsum = part + 2 * (OT + 1);
-  uint16_t* cnt = reinterpret_cast<uint16_t*>(wsum + OW);   // [OW][N]; at most kRound
+  int32_t* tot = base + pitch;       // all pairs of each expert
+  int32_t* sub = tot + pitch;        // the round's
+  int32_t* wsum = sub + pitch;
+  int32_t* part = wsum + OW;         // [2][slices][pitch]
+  uint16_t* cnt = reinterpret_cast<uint16_t*>(part);   // [OW][N]; at most kRound
   const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
   uint16_t* mine = cnt + (size_t)wave * N;
   const int64_t from = blockIdx.x * tile, to = from + tile < pairs ? from + tile : pairs;
@@ -721,31 +728,34 @@ __global__ __launch_bounds__(OT) void order_place(int64_t pairs, int64_t tile, i
   while ((1 << bits) <= E) ++bits;
 
   if (tiles > 1) {
-    // pairs of each expert in the tiles before this one and in all: slices of
-    // the tiles side by side, as many as fit the workgroup
-    const int slices = OT / N > 0 ? OT / N : 1;
-    for (int i = threadIdx.x; i < slices * N; i += OT) {   // i < OT, or N = OT + 1
-      const int e = i % N, s0 = i / N;
-      int before = 0, all = 0;
+    // pairs of each expert in the tiles before this one and in all: four
+    // experts a lane, slices of the tiles side by side
+    typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+    const int quads = pitch / 4, slices = OT / quads;   // at most 257 quads
+    const int quad = threadIdx.x % quads, slice = threadIdx.x / quads;
+    i32x4* sums = reinterpret_cast<i32x4*>(part);
+    if (slice < slices) {
+      i32x4 before = {}, all = {};
 #pragma unroll 8
-      for (int t = s0; t < tiles; t += slices) {
-        const int n = hist[t * (int64_t)N + e];
+      for (int t = slice; t < tiles; t += slices) {
+        const i32x4 n = reinterpret_cast<const i32x4*>(hist)[t * (int64_t)quads + quad];
         all += n;
-        before += t < (int)blockIdx.x ? n : 0;
+        if (t < (int)blockIdx.x) before += n;
       }
-      part[i] = before;
-      part[OT + 1 + i] = all;
+      sums[slice * quads + quad] = before;
+      sums[(slices + slice) * quads + quad] = all;
     }
     __syncthreads();
     for (int e = threadIdx.x; e < N; e += OT) {
       int before = 0, all = 0;
       for (int q = 0; q < slices; ++q) {
-        before += part[q * N + e];
-        all += part[OT + 1 + q * N + e];
+        before += part[q * pitch + e];
+        all += part[(slices + q) * pitch + e];
       }
       base[e] = before;
       tot[e] = all;
     }
+    __syncthreads();
   }
 
   for (int64_t p0 = from; p0 < to; p0 += kRound) {
@@ -921,8 +931,8 @@ hipError_t run_route_order(int64_t pairs, int64_t experts_n, const int32_t* expe
     return hipGetLastError();
   }
   if (tiles > 1) {
-    MUON_LAUNCH_SHM("order_count", order_count, dim3((unsigned)tiles), dim3(OT), size_t(E + 1) * 4, stream, pairs, tile,
-                    E, experts, ws);
+    MUON_LAUNCH_SHM("order_count", order_count, dim3((unsigned)tiles), dim3(OT), size_t(order_pitch(E)) * 4, stream, pairs,
+                    tile, E, experts, ws);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
