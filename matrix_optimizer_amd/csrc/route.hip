@@ -213,10 +213,12 @@ __device__ __forceinline__ void load_logits(const T* row, int E, int t, float* l
     const int c = (i * LPT + t) * 8;
     load8(row, c, E, l + 8 * i);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      l[8 * i + j] = read_logit(l[8 * i + j]);
-      if (c + j >= E) l[8 * i + j] = -HUGE_VALF;
-    }
+    for (int j = 0; j < 8; ++j) l[8 * i + j] = read_logit(l[8 * i + j]);
+  }
+  if (E < LPT * NC * 8) {
+#pragma unroll
+    for (int i = 0; i < 8 * NC; ++i)
+      if (((i / 8) * LPT + t) * 8 + i % 8 >= E) l[i] = -HUGE_VALF;
   }
 }
 
@@ -276,10 +278,15 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
   const T* row = static_cast<const T*>(a.logits) + r * a.logits_stride;
   float l[V];
   load_logits<T, LPT, NC>(row, E, t, l);
-  float top = l[0];
+  float top = l[0], least = l[0];
 #pragma unroll
-  for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
-  top = over_row<LPT>(top, max_f);
+  for (int i = 1; i < V; ++i) least = fminf(least, l[i]);
+  const bool shut = __any(!(least > -HUGE_VALF));   // an expert of the wave's rows is closed
+  if (soft) {
+#pragma unroll
+    for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
+    top = over_row<LPT>(top, max_f);
+  }
   float z = 1.f;
   float v[V];            // what is ranked; -inf: may not be chosen
   // Bound on the error of the difference of two scores.  Sigmoid: the fast exp
@@ -330,11 +337,12 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
         for (int j = 0; j < 8; ++j) v[8 * i + j] += b[j];
       }
     }
+    if (shut) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = l[i] > -HUGE_VALF ? v[i] : -HUGE_VALF;
+      for (int i = 0; i < V; ++i) v[i] = l[i] > -HUGE_VALF ? v[i] : -HUGE_VALF;
+    }
   }
   bool unsure = false;   // grade 3
-  uint32_t in = ~0u;     // bit i: element i's group stays
   if (G > 1) {
     float* by_l = wave_lds + (size_t)(lane / LPT) * (E + 2 * G);
     float* of_l = by_l + E;
@@ -399,31 +407,32 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
       in_l[g] = sure < s.top_groups;
     }
     wave_sync();
+    if (!a.bias) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = l[i];
+    }
     if (lanes) {
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int g = (i * LPT + t) / span;
-        if (g < G && !in_l[g]) in &= ~(0xffu << (8 * i));
+        const bool out = g < G && !in_l[g];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[8 * i + j] = out ? -HUGE_VALF : v[8 * i + j];
       }
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int e = ((i / 8) * LPT + t) * 8 + i % 8;
-        if (e < E && !in_l[e / n]) in &= ~(1u << i);
+        if (e < E && !in_l[e / n]) v[i] = -HUGE_VALF;
       }
     }
-  }
-  if (!a.bias) {
+  } else if (!a.bias) {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = l[i];
   }
-  if (G > 1) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = (in >> i) & 1 ? v[i] : -HUGE_VALF;
-  }
 
   // grade 1
-  constexpr int kIndex = MUON_ROUTE_MAX_EXPERTS - 1, kLow = -(1 << 21);
+  constexpr int kIndex = MUON_ROUTE_MAX_EXPERTS - 1, kLow = 1 - (1 << 21);
   const bool whole = !a.bias && sizeof(T) == 2;
   bool open = false;     // grade 2
   int cands = 0;         // experts in `chosen`, more than K where the last's value is not apart
@@ -434,19 +443,32 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
     // largest, of 2^-20 in a range of 2 for scores and of 2^-17 in 32 for
     // logits; values are in order where their steps differ, and scores where
     // these differ by `apart`
-    float most = v[0];
+    const int low = (~t & (LPT - 1)) * 8;   // 1023 - e in bits: those of t, chunk and element reversed
+    int apart = 0;
+    if (whole) {
 #pragma unroll
-    for (int i = 1; i < V; ++i) most = fmaxf(most, v[i]);
-    most = over_row<LPT>(most, max_f);
-    const float by = a.bias ? 0x1p20f : 0x1p17f;
-    const int apart = a.bias ? (int)fminf(2.f + 0x1p20f * (tol + 0x1p-22f * (fabsf(most) + 2.f)), 0x1p22f) : 0;
+      for (int i = 0; i < V; ++i) num[i] = key_of(v[i]) & ~kIndex;
+    } else {
+      float most = v[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) most = fmaxf(most, v[i]);
+      most = over_row<LPT>(most, max_f);
+      const float by = a.bias ? 0x1p20f : 0x1p17f;
+      if (a.bias) apart = (int)fminf(2.f + by * (tol + 0x1p-22f * (fabsf(most) + 2.f)), 0x1p22f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) num[i] = (int)fmaxf((v[i] - most) * by, (float)kLow) * (kIndex + 1);
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = ((i / 8) * LPT + t) * 8 + i % 8;
-      const int q = whole ? key_of(v[i]) >> 10 : (int)fmaxf((v[i] - most) * by, (float)kLow);
-      num[i] = v[i] > -HUGE_VALF ? q * (kIndex + 1) + (kIndex - e) : kNone;
-      m = max_i(m, num[i]);
+      constexpr int upper = kIndex & ~(LPT * 8 - 1);
+      num[i] = num[i] | low | ((upper - (i / 8) * LPT * 8) + (7 - i % 8));
     }
+    if (shut || G > 1) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) num[i] = v[i] > -HUGE_VALF ? num[i] : kNone;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = max_i(m, num[i]);
     m = over_row<LPT>(m, max_i);
     auto next = [&](int m) {   // the largest number below m; no number stays none
       uint32_t d = ~0u;
@@ -700,13 +722,35 @@ __global__ __launch_bounds__(OT) void order_count(int64_t pairs, int64_t tile, i
   for (int e = threadIdx.x; e < pitch; e += OT) hist[blockIdx.x * (int64_t)pitch + e] = lds_i[e];
 }
 
-// Shared memory of order_place, in 4-byte words: base, tot and sub of E + 1
-// each, OW wave sums, and, one after the other, the partial sums over the
-// tiles (a 16-byte piece of two kinds a lane) and a 16-bit count a wave and
-// expert.
+// Shared memory of order_place, in 4-byte words: base, tot, sub and loc of
+// E + 1 each, OW wave sums, a 16-byte piece of two kinds a lane (the sums over
+// the tiles, then the round's pairs and places in order), and a 16-bit count a
+// wave and expert.
 __host__ __device__ constexpr int order_words(int E) {
-  const int sums = 2 * 4 * OT, cnt = (OW * (E + 1) + 1) / 2;
-  return 3 * order_pitch(E) + OW + (sums > cnt ? sums : cnt);
+  return 4 * order_pitch(E) + OW + 2 * (int)kRound + (OW * (E + 1) + 1) / 2;
+}
+
+// Exclusive sum over the workgroup in lane order; `total` of all.
+__device__ __forceinline__ int group_scan(int v, int32_t* wsum, int& total) {
+  const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
+  int run = v;
+#pragma unroll
+  for (int o = 1; o < WAVE; o <<= 1) {
+    const int up = __shfl_up(run, o, WAVE);
+    run += lane >= o ? up : 0;
+  }
+  if (lane == WAVE - 1) wsum[wave] = run;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < OW; ++w) {
+    const int n = wsum[w];
+    before += w < wave ? n : 0;
+    total += n;
+  }
+  __syncthreads();
+  return before + run - v;
 }
 
 __global__ __launch_bounds__(OT) void order_place(int64_t pairs, int64_t tile, int E, int tiles, const int32_t* experts,
@@ -718,14 +762,28 @@ __global__ __launch_bounds__(OT) void order_place(int64_t pairs, int64_t tile, i
   int32_t* base = lds_i;             // place of the round's first pair of each expert
   int32_t* tot = base + pitch;       // all pairs of each expert
   int32_t* sub = tot + pitch;        // the round's
-  int32_t* wsum = sub + pitch;
-  int32_t* part = wsum + OW;         // [2][slices][pitch]
-  uint16_t* cnt = reinterpret_cast<uint16_t*>(part);   // [OW][N]; at most kRound
+  int32_t* loc = sub + pitch;        // place of its first one in the round
+  int32_t* wsum = loc + pitch;
+  int32_t* part = wsum + OW;         // [2][slices][pitch], then the round's pairs and places
+  uint16_t* cnt = reinterpret_cast<uint16_t*>(part + 2 * kRound);   // [OW][N]; at most kRound
   const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
   uint16_t* mine = cnt + (size_t)wave * N;
-  const int64_t from = blockIdx.x * tile, to = from + tile < pairs ? from + tile : pairs;
+  // neighbouring tiles write the two halves of a cache line: on one XCD
+  const int me = (blockIdx.x & 7) * (gridDim.x / 8) + blockIdx.x / 8;
+  if (me >= tiles) return;
+  const int64_t from = me * tile, to = from + tile < pairs ? from + tile : pairs;
   int bits = 1;
   while ((1 << bits) <= E) ++bits;
+
+  int ex[kChunks];
+  auto fetch = [&](int64_t p0) {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int64_t p = p0 + (int64_t)(wave * kChunks + c) * WAVE + lane;
+      ex[c] = p < to ? read_expert(experts, p, E) : -1;
+    }
+  };
+  fetch(from);
 
   if (tiles > 1) {
     // pairs of each expert in the tiles before this one and in all: four
@@ -735,19 +793,20 @@ __global__ __launch_bounds__(OT) void order_place(int64_t pairs, int64_t tile, i
     const int quad = threadIdx.x % quads, slice = threadIdx.x / quads;
     i32x4* sums = reinterpret_cast<i32x4*>(part);
     if (slice < slices) {
-      i32x4 before = {}, all = {};
+      i32x4 before = {}, after = {};
+      const i32x4* h = reinterpret_cast<const i32x4*>(hist) + quad;
+      int t = slice;
 #pragma unroll 8
-      for (int t = slice; t < tiles; t += slices) {
-        const i32x4 n = reinterpret_cast<const i32x4*>(hist)[t * (int64_t)quads + quad];
-        all += n;
-        if (t < (int)blockIdx.x) before += n;
-      }
+      for (; t < me; t += slices) before += h[t * quads];   // at most 256 tiles of 257 pieces
+#pragma unroll 8
+      for (; t < tiles; t += slices) after += h[t * quads];
       sums[slice * quads + quad] = before;
-      sums[(slices + slice) * quads + quad] = all;
+      sums[(slices + slice) * quads + quad] = before + after;
     }
     __syncthreads();
     for (int e = threadIdx.x; e < N; e += OT) {
       int before = 0, all = 0;
+#pragma unroll 4
       for (int q = 0; q < slices; ++q) {
         before += part[q * pitch + e];
         all += part[(slices + q) * pitch + e];
@@ -755,24 +814,23 @@ __global__ __launch_bounds__(OT) void order_place(int64_t pairs, int64_t tile, i
       base[e] = before;
       tot[e] = all;
     }
-    __syncthreads();
   }
 
   for (int64_t p0 = from; p0 < to; p0 += kRound) {
-    for (int i = threadIdx.x; i < OW * N; i += OT) cnt[i] = 0;
-    int ex[kChunks], rank[kChunks];
-    const int64_t first = p0 + (int64_t)wave * (kChunks * WAVE) + lane;
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) ex[c] = first + c * WAVE < to ? read_expert(experts, first + c * WAVE, E) : -1;
+    for (int i = threadIdx.x; i < (OW * N + 1) / 2; i += OT) reinterpret_cast<int32_t*>(cnt)[i] = 0;
+    int rank[kChunks];
     __syncthreads();
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      uint64_t same = __ballot(ex[c] >= 0);
+      const uint64_t there = __ballot(ex[c] >= 0);
+      uint32_t lo = (uint32_t)there, hi = (uint32_t)(there >> 32);
       for (int b = 0; b < bits; ++b) {
-        const bool bit = (ex[c] >> b) & 1;
-        const uint64_t m = __ballot(bit);
-        same &= bit ? m : ~m;
+        const int bit = -((ex[c] >> b) & 1);   // all ones or zero
+        const uint64_t m = __ballot(bit != 0);
+        lo &= ~((uint32_t)m ^ (uint32_t)bit);
+        hi &= ~((uint32_t)(m >> 32) ^ (uint32_t)bit);
       }
+      const uint64_t same = (uint64_t)hi << 32 | lo;
       const int before = __popcll(same & ((uint64_t(1) << lane) - 1));
       const int so_far = ex[c] >= 0 ? mine[ex[c]] : 0;
       rank[c] = so_far + before;
@@ -796,45 +854,44 @@ __global__ __launch_bounds__(OT) void order_place(int64_t pairs, int64_t tile, i
       }
     }
     __syncthreads();
-    if (p0 == from) {
-      // the experts' first places: exclusive sums of the totals, E <= OT
-      const int v = (int)threadIdx.x < E ? tot[threadIdx.x] : 0;
-      int run = v;
-#pragma unroll
-      for (int o = 1; o < WAVE; o <<= 1) {
-        const int up = __shfl_up(run, o, WAVE);
-        run += lane >= o ? up : 0;
-      }
-      if (lane == WAVE - 1) wsum[wave] = run;
-      __syncthreads();
-      int before = 0, total = 0;
-#pragma unroll
-      for (int w = 0; w < OW; ++w) {
-        before += w < wave ? wsum[w] : 0;
-        total += wsum[w];
-      }
-      if ((int)threadIdx.x < E) {
-        base[threadIdx.x] += before + run - v;
-        if (blockIdx.x == 0) {
-          offsets[threadIdx.x] = before + run - v;
-          counts[threadIdx.x] = v;
+    const int e0 = threadIdx.x;   // E <= OT
+    int total;
+    const int inside = group_scan(e0 < E ? sub[e0] : 0, wsum, total);
+    if (e0 < E) loc[e0] = inside;
+    if (e0 == 0) loc[E] = total;
+    if (p0 == from) {   // the experts' first places
+      const int v = e0 < E ? tot[e0] : 0;
+      const int first = group_scan(v, wsum, total);
+      if (e0 < E) base[e0] += first;
+      if (e0 == 0) base[E] += total;
+      if (me == 0) {
+        if (e0 < E) {
+          offsets[e0] = first;
+          counts[e0] = v;
         }
+        if (e0 == 0) offsets[E] = total;
       }
-      if (threadIdx.x == 0) {
-        base[E] += total;
-        if (blockIdx.x == 0) offsets[E] = total;
-      }
-      __syncthreads();
-    }
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int e = ex[c];
-      if (e < 0) continue;
-      const int place = base[e] + (int)mine[e] + rank[c];
-      order[place] = e < E ? (int32_t)(first + c * WAVE) : -1;
-      position[first + c * WAVE] = e < E ? place : -1;
     }
     __syncthreads();
+    // pairs and places in the round's order, so that a wave's stores to
+    // `order` are a few runs and not 64 lines
+    int2* sorted = reinterpret_cast<int2*>(part);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int64_t p = p0 + (int64_t)(wave * kChunks + c) * WAVE + lane;
+      const int e = ex[c];
+      if (e < 0) continue;
+      const int at = (int)mine[e] + rank[c], place = base[e] + at;
+      sorted[loc[e] + at] = make_int2(e < E ? (int)p : -1, place);
+      position[p] = e < E ? place : -1;
+    }
+    if (p0 + kRound < to) fetch(p0 + kRound);
+    __syncthreads();
+    const int n = (int)(to - p0 < kRound ? to - p0 : kRound);
+    for (int i = threadIdx.x; i < n; i += OT) {
+      const int2 x = sorted[i];
+      order[x.y] = x.x;
+    }
     for (int e = threadIdx.x; e < N; e += OT) base[e] += sub[e];
     __syncthreads();
   }
@@ -936,7 +993,7 @@ hipError_t run_route_order(int64_t pairs, int64_t experts_n, const int32_t* expe
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  MUON_LAUNCH_SHM("order_place", order_place, dim3((unsigned)tiles), dim3(OT), size_t(order_words(E)) * 4, stream, pairs,
+  MUON_LAUNCH_SHM("order_place", order_place, dim3((unsigned)(tiles + 7) / 8 * 8), dim3(OT), size_t(order_words(E)) * 4, stream, pairs,
                   tile, E, (int)tiles, experts, ws, counts, offsets, order, position);
   return hipGetLastError();
 }
