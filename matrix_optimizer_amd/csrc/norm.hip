@@ -32,7 +32,8 @@ __global__ __launch_bounds__(NT) void dropout_k(int64_t rows, int64_t cols, cons
 }
 
 // Columns c .. c+7 of weight (ones without one).
-__device__ __forceinline__ void weight8(const void* w, int dtype, int64_t c, int64_t cols, float* f) {
+template <class I>
+__device__ __forceinline__ void weight8(const void* w, int dtype, I c, I cols, float* f) {
   if (!w) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = 1.f;
@@ -65,12 +66,12 @@ __device__ __forceinline__ float scale_of(float most, float top) {
 // y of columns c .. c+7 at its type; an 8-bit y with the group's scale, found
 // across the group's lanes unless the row's is given.  LPR: lanes of a row if
 // fewer than a wave (a group then ends with the row).
-template <int LPR>
-__device__ __forceinline__ void store_y(const muon_norm_args& a, int64_t r, int64_t c, float* y, float row_scale) {
+template <int LPR, class I>
+__device__ __forceinline__ void store_y(const muon_norm_args& a, int64_t r, I c, I cols, float* y, float row_scale) {
   if (a.y_dtype == MUON_ROW_F32) {
-    if (c < a.cols) store8(static_cast<float*>(a.y) + r * a.y_stride, c, a.cols, y);
+    if (c < cols) store8(static_cast<float*>(a.y) + r * a.y_stride, c, cols, y);
   } else if (a.y_dtype == MUON_ROW_BF16) {
-    if (c < a.cols) store8(static_cast<bf16_t*>(a.y) + r * a.y_stride, c, a.cols, y);
+    if (c < cols) store8(static_cast<bf16_t*>(a.y) + r * a.y_stride, c, cols, y);
   } else {
     const bool e5 = a.y_dtype == MUON_ROW_E5M2;
     float scale = row_scale;
@@ -80,15 +81,15 @@ __device__ __forceinline__ void store_y(const muon_norm_args& a, int64_t r, int6
       for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(y[j]));
       for (int o = LPR ? min(a.group / 16, LPR / 2) : a.group / 16; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, WAVE));
       scale = scale_of(most, e5 ? 57344.f : 448.f);
-      if (c < a.cols && (c & (a.group - 1)) == 0) a.scales[r * a.scales_stride + c / a.group] = scale;
+      if (c < cols && (c & (a.group - 1)) == 0) a.scales[r * a.scales_stride + c / a.group] = scale;
     }
     const float inv = 1.f / scale;
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] *= inv;
     uint8_t* row = static_cast<uint8_t*>(a.y) + r * a.y_stride;
-    if (c < a.cols) {
-      if (e5) store8_8bit<true>(row, c, a.cols, y);
-      else store8_8bit<false>(row, c, a.cols, y);
+    if (c < cols) {
+      if (e5) store8_8bit<true>(row, c, cols, y);
+      else store8_8bit<false>(row, c, cols, y);
     }
   }
 }
@@ -142,6 +143,7 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_fwd(muon_norm_args a, Dro
     red_init(maxima);
   }
   const RowLanes<LPR> at;
+  const int cols = (int)a.cols;
   const int lanes = at.lanes, t = at.t;
   const int64_t step = at.step;
   int64_t r = at.r;
@@ -153,11 +155,11 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_fwd(muon_norm_args a, Dro
   Chunk<T> cx[NC], cr[NC];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    const int64_t c = (int64_t)(i * lanes + t) * 8;
-    weight8(a.weight, a.weight_dtype, c, a.cols, w[i]);
+    const int c = (i * lanes + t) * 8;
+    weight8(a.weight, a.weight_dtype, c, cols, w[i]);
     if (r < a.rows) {
-      cx[i].load(x + r * a.x_stride, c, a.cols);
-      if (res) cr[i].load(res + r * a.residual_stride, c, a.cols);
+      cx[i].load(x + r * a.x_stride, c, cols);
+      if (res) cr[i].load(res + r * a.residual_stride, c, cols);
     }
   }
   for (int turn = 0; r < a.rows; r += step, turn ^= 1) {
@@ -165,7 +167,7 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_fwd(muon_norm_args a, Dro
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int64_t c = (int64_t)(i * lanes + t) * 8;
+      const int c = (i * lanes + t) * 8;
       cx[i].get(z[i]);
       if (d.on) drop8(d, seed, offset, r, c, z[i]);
       if (res) {
@@ -180,19 +182,19 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_fwd(muon_norm_args a, Dro
     if (r + step < a.rows) {
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int64_t c = (int64_t)(i * lanes + t) * 8;
-        cx[i].load(x + (r + step) * a.x_stride, c, a.cols);
-        if (res) cr[i].load(res + (r + step) * a.residual_stride, c, a.cols);
+        const int c = (i * lanes + t) * 8;
+        cx[i].load(x + (r + step) * a.x_stride, c, cols);
+        if (res) cr[i].load(res + (r + step) * a.residual_stride, c, cols);
       }
     }
     ss = LPR ? lanes_sum<LPR>(ss) : group_sum(ss, sums, turn);
-    const float rstd = 1.f / sqrtf(ss / (float)a.cols + a.eps);
+    const float rstd = 1.f / sqrtf(ss / (float)cols + a.eps);
     if (a.rstd && t == 0) a.rstd[r] = rstd;
     if (a.h) {
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int64_t c = (int64_t)(i * lanes + t) * 8;
-        if (c < a.cols) store8(static_cast<T*>(a.h) + r * a.h_stride, c, a.cols, z[i]);
+        const int c = (i * lanes + t) * 8;
+        if (c < cols) store8(static_cast<T*>(a.h) + r * a.h_stride, c, cols, z[i]);
       }
     }
     float most = 0.f;
@@ -210,7 +212,7 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_fwd(muon_norm_args a, Dro
       if (t == 0) a.scales[r * a.scales_stride] = row_scale;
     }
 #pragma unroll
-    for (int i = 0; i < NC; ++i) store_y<LPR>(a, r, (int64_t)(i * lanes + t) * 8, z[i], row_scale);
+    for (int i = 0; i < NC; ++i) store_y<LPR>(a, r, (i * lanes + t) * 8, cols, z[i], row_scale);
   }
 }
 
@@ -260,7 +262,7 @@ __global__ __launch_bounds__(512) void norm_fwd_long(muon_norm_args a, Drop d) {
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) y[j] = in && c + j < a.cols ? z[j] * rstd * w[j] : 0.f;
-      store_y<0>(a, r, c, y, row_scale);
+      store_y<0>(a, r, c, a.cols, y, row_scale);
     }
   }
 }
@@ -273,6 +275,7 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_bwd(muon_norm_grad_args a
   __shared__ GroupRed sums;
   if constexpr (LPR == 0) red_init(sums);
   const RowLanes<LPR> at;
+  const int cols = (int)a.cols;
   const int lanes = at.lanes, t = at.t;
   const int64_t step = at.step;
   int64_t r = at.r;
@@ -290,15 +293,15 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_bwd(muon_norm_grad_args a
     rstd = a.rstd[row];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int64_t c = (int64_t)(i * lanes + t) * 8;
-      cg[i].load(dy + row * a.dy_stride, c, a.cols);
-      ch[i].load(h + row * a.h_stride, c, a.cols);
-      if (dh) cd[i].load(dh + row * a.dh_stride, c, a.cols);
+      const int c = (i * lanes + t) * 8;
+      cg[i].load(dy + row * a.dy_stride, c, cols);
+      ch[i].load(h + row * a.h_stride, c, cols);
+      if (dh) cd[i].load(dh + row * a.dh_stride, c, cols);
     }
   };
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    weight8(a.weight, a.weight_dtype, (int64_t)(i * lanes + t) * 8, a.cols, w[i]);
+    weight8(a.weight, a.weight_dtype, (i * lanes + t) * 8, cols, w[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
   }
@@ -323,11 +326,11 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_bwd(muon_norm_grad_args a
       }
     }
     if (AHEAD && r + step < a.rows) fetch(r + step);
-    const float mean = (LPR ? lanes_sum<LPR>(dot) : group_sum(dot, sums, turn)) / (float)a.cols;
+    const float mean = (LPR ? lanes_sum<LPR>(dot) : group_sum(dot, sums, turn)) / (float)cols;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int64_t c = (int64_t)(i * lanes + t) * 8;
-      if (c >= a.cols) continue;
+      const int c = (i * lanes + t) * 8;
+      if (c >= cols) continue;
 #pragma unroll
       for (int j = 0; j < 8; ++j) g[i][j] = rs * (g[i][j] - xh[i][j] * mean);
       if (dh) {
@@ -336,15 +339,15 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_bwd(muon_norm_grad_args a
 #pragma unroll
         for (int j = 0; j < 8; ++j) g[i][j] += f[j];
       }
-      if (a.dresidual) store8(static_cast<T*>(a.dresidual) + r * a.dresidual_stride, c, a.cols, g[i]);
+      if (a.dresidual) store8(static_cast<T*>(a.dresidual) + r * a.dresidual_stride, c, cols, g[i]);
       if (a.dx) {
         if (d.on) drop8(d, seed, offset, r, c, g[i]);
-        store8(static_cast<T*>(a.dx) + r * a.dx_stride, c, a.cols, g[i]);
+        store8(static_cast<T*>(a.dx) + r * a.dx_stride, c, cols, g[i]);
       }
     }
   }
   if (!a.dweight) return;
-  float* out = gridDim.x == 1 ? a.dweight : parts + blockIdx.x * a.cols;
+  float* out = gridDim.x == 1 ? a.dweight : parts + blockIdx.x * (int64_t)cols;
   if constexpr (LPR != 0) {
     // the rows a workgroup worked on side by side, added in their order
     constexpr int rows = NT / (LPR ? LPR : 1);
@@ -356,17 +359,17 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_bwd(muon_norm_grad_args a
     __syncthreads();
     for (int q = threadIdx.x; q < NC * 8 * LPR; q += NT) {
       const int k = q / LPR, lane = q % LPR;   // chunk k / 8 of that lane, its column k % 8
-      const int64_t c = (int64_t)((k / 8) * LPR + lane) * 8 + k % 8;
+      const int c = ((k / 8) * LPR + lane) * 8 + k % 8;
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < rows; ++w) v += all[w][k][lane];
-      if (c < a.cols) out[c] = v;
+      if (c < cols) out[c] = v;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int64_t c = (int64_t)(i * lanes + t) * 8;
-      if (c < a.cols) store8(out, c, a.cols, dw[i]);
+      const int c = (i * lanes + t) * 8;
+      if (c < cols) store8(out, c, cols, dw[i]);
     }
   }
 }
@@ -483,6 +486,14 @@ RowShape row_shape(int64_t cols) {
   return {0, nc, (unsigned)round_up((chunks + nc - 1) / nc, WAVE), 1};
 }
 
+// Workgroups for `groups` of rows, at most `most` and all with as many rows as
+// the others but the last few.
+int64_t even(int64_t groups, int64_t most) {
+  if (groups < 1) return 0;
+  const int64_t each = (groups + most - 1) / most;
+  return (groups + each - 1) / each;
+}
+
 // Forward: workgroups that stay on the GPU, 1024 lanes on each of 256 CUs.
 // [16384, 4096] bf16 with p = 0.1: 105 us, 111 with twice as many (the last
 // round of workgroups is then part empty), 111 with half.
@@ -493,11 +504,12 @@ int64_t resident(unsigned threads) { return 256 * std::max(1u, 1024 / threads); 
 // Backward: each workgroup leaves a row of partial sums, written and read
 // again.  Two workgroups a CU where a lane keeps one chunk ([16384, 4096] with
 // dropout: 110 us, one 117, four 124), one where it keeps more ([4096, 8192]:
-// 43 us, two 48) and where two would leave fewer than 8 rows to each.
+// 43 us, two 48) and where two would leave fewer than 8 rows to each; up to 4
+// rows in a row a single one, which needs no second launch.
 int64_t norm_parts(int64_t rows, int64_t cols) {
   const RowShape s = row_shape(cols);
   const int64_t groups = (rows + s.per_group - 1) / s.per_group;
-  return std::min<int64_t>(groups, s.nc == 1 && groups >= 4096 ? 512 : 256);
+  return groups <= 4 ? std::min<int64_t>(groups, 1) : even(groups, s.nc == 1 && groups >= 4096 ? 512 : 256);
 }
 
 hipError_t run_dropout(int64_t rows, int64_t cols, const void* x, int64_t xs, void* y, int64_t ys, int dtype,
@@ -517,7 +529,7 @@ template <typename T>
 static void launch_forward(const muon_norm_args& a, const Drop& d, hipStream_t stream) {
   const RowShape s = row_shape(a.cols);
   const int64_t groups = (a.rows + s.per_group - 1) / s.per_group;
-  const dim3 grid((unsigned)std::min(groups, resident(s.threads))), block(s.threads);
+  const dim3 grid((unsigned)even(groups, resident(s.threads))), block(s.threads);
   if (s.lpr == 8) MUON_LAUNCH("norm_fwd", (norm_fwd<T, 1, 8>), grid, block, stream, a, d);
   else if (s.lpr == 16) MUON_LAUNCH("norm_fwd", (norm_fwd<T, 1, 16>), grid, block, stream, a, d);
   else if (s.lpr == 32) MUON_LAUNCH("norm_fwd", (norm_fwd<T, 1, 32>), grid, block, stream, a, d);
@@ -539,7 +551,7 @@ template <typename T>
 static void launch_backward(const muon_norm_grad_args& a, const Drop& d, float* parts, hipStream_t stream) {
   const RowShape s = row_shape(a.cols);
   const int64_t groups = (a.rows + s.per_group - 1) / s.per_group;
-  const dim3 grid((unsigned)(a.dweight ? norm_parts(a.rows, a.cols) : std::min(groups, resident(s.threads))));
+  const dim3 grid((unsigned)(a.dweight ? norm_parts(a.rows, a.cols) : even(groups, resident(s.threads))));
   const dim3 block(s.threads);
   if (s.lpr == 8) MUON_LAUNCH("norm_bwd", (norm_bwd<T, 1, 8>), grid, block, stream, a, d, parts);
   else if (s.lpr == 16) MUON_LAUNCH("norm_bwd", (norm_bwd<T, 1, 16>), grid, block, stream, a, d, parts);

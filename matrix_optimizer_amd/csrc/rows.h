@@ -22,13 +22,18 @@ __device__ __forceinline__ void unpack8(const u32x4& v, float* f) {
 
 // Columns c .. c+7 of a row in their stored form, zeros from column `cols` on
 // (c may lie past it): 4 registers of bf16 or 8 of fp32, so that loads can be
-// in flight while the row before is worked on.
+// in flight while the row before is worked on.  Lanes past the row's end skip
+// the columns one by one: a wave with idle lanes at the end of a row would
+// otherwise be the slowest ([3777, 2880] bf16 by 384 lanes: 30 us, 18 without).
 template <typename T> struct Chunk;
 template <> struct Chunk<bf16_t> {
   u32x4 v;
-  __device__ __forceinline__ void load(const bf16_t* row, int64_t c, int64_t cols) {
+  template <class I>
+  __device__ __forceinline__ void load(const bf16_t* row, I c, I cols) {
     if (c + 8 <= cols) {
       v = *reinterpret_cast<const u32x4_any*>(row + c);
+    } else if (c >= cols) {
+      v = u32x4{};
     } else {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -41,10 +46,14 @@ template <> struct Chunk<bf16_t> {
 };
 template <> struct Chunk<float> {
   u32x4 a, b;
-  __device__ __forceinline__ void load(const float* row, int64_t c, int64_t cols) {
+  template <class I>
+  __device__ __forceinline__ void load(const float* row, I c, I cols) {
     if (c + 8 <= cols) {
       a = *reinterpret_cast<const u32x4_any*>(row + c);
       b = *reinterpret_cast<const u32x4_any*>(row + c + 4);
+    } else if (c >= cols) {
+      a = u32x4{};
+      b = u32x4{};
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -62,8 +71,8 @@ template <> struct Chunk<float> {
   }
 };
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* row, int64_t c, int64_t cols, float* f) {
+template <typename T, class I>
+__device__ __forceinline__ void load8(const T* row, I c, I cols, float* f) {
   Chunk<T> k;
   k.load(row, c, cols);
   k.get(f);
@@ -74,7 +83,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // The same columns rounded and stored; those from `cols` on are left alone.
-__device__ __forceinline__ void store8(bf16_t* row, int64_t c, int64_t cols, const float* f) {
+template <class I>
+__device__ __forceinline__ void store8(bf16_t* row, I c, I cols, const float* f) {
   if (c + 8 <= cols) {
     u32x4 v;
 #pragma unroll
@@ -86,7 +96,8 @@ __device__ __forceinline__ void store8(bf16_t* row, int64_t c, int64_t cols, con
       if (c + j < cols) row[c + j] = f2bf(f[j]);
   }
 }
-__device__ __forceinline__ void store8(float* row, int64_t c, int64_t cols, const float* f) {
+template <class I>
+__device__ __forceinline__ void store8(float* row, I c, I cols, const float* f) {
   if (c + 8 <= cols) {
     u32x4 a, b;
 #pragma unroll
@@ -108,8 +119,8 @@ __device__ __forceinline__ float limit(float v, float top) { return v > top ? to
 
 // Eight values (already divided by their scale) in an 8-bit format, rounded
 // to nearest even.
-template <bool E5M2>
-__device__ __forceinline__ void store8_8bit(uint8_t* row, int64_t c, int64_t cols, const float* f) {
+template <bool E5M2, class I>
+__device__ __forceinline__ void store8_8bit(uint8_t* row, I c, I cols, const float* f) {
   constexpr float top = E5M2 ? 57344.f : 448.f;
   float v[8];
 #pragma unroll
