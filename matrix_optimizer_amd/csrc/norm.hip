@@ -494,10 +494,13 @@ int64_t even(int64_t groups, int64_t most) {
   return (groups + each - 1) / each;
 }
 
-// Forward: workgroups that stay on the GPU, 1024 lanes on each of 256 CUs.
+// Forward: workgroups that stay on the GPU, at least 1024 lanes on each of 256
+// CUs where a lane keeps one chunk, two workgroups where it keeps more.
 // [16384, 4096] bf16 with p = 0.1: 105 us, 111 with twice as many (the last
-// round of workgroups is then part empty), 111 with half.
-int64_t resident(unsigned threads) { return 256 * std::max(1u, 1024 / threads); }
+// round of workgroups is then part empty), 111 with half; [3777, 2880] by
+// three workgroups of 384 lanes 20 us, by two or four 24 (a fourth does not fit
+// the SIMD that holds two waves of each).
+int64_t resident(const RowShape& s) { return 256 * (s.nc == 1 ? (1024 + s.threads - 1) / s.threads : 1024 / s.threads); }
 
 }  // namespace
 
@@ -529,7 +532,7 @@ template <typename T>
 static void launch_forward(const muon_norm_args& a, const Drop& d, hipStream_t stream) {
   const RowShape s = row_shape(a.cols);
   const int64_t groups = (a.rows + s.per_group - 1) / s.per_group;
-  const dim3 grid((unsigned)even(groups, resident(s.threads))), block(s.threads);
+  const dim3 grid((unsigned)even(groups, resident(s))), block(s.threads);
   if (s.lpr == 8) MUON_LAUNCH("norm_fwd", (norm_fwd<T, 1, 8>), grid, block, stream, a, d);
   else if (s.lpr == 16) MUON_LAUNCH("norm_fwd", (norm_fwd<T, 1, 16>), grid, block, stream, a, d);
   else if (s.lpr == 32) MUON_LAUNCH("norm_fwd", (norm_fwd<T, 1, 32>), grid, block, stream, a, d);
@@ -551,7 +554,7 @@ template <typename T>
 static void launch_backward(const muon_norm_grad_args& a, const Drop& d, float* parts, hipStream_t stream) {
   const RowShape s = row_shape(a.cols);
   const int64_t groups = (a.rows + s.per_group - 1) / s.per_group;
-  const dim3 grid((unsigned)(a.dweight ? norm_parts(a.rows, a.cols) : even(groups, resident(s.threads))));
+  const dim3 grid((unsigned)(a.dweight ? norm_parts(a.rows, a.cols) : even(groups, resident(s))));
   const dim3 block(s.threads);
   if (s.lpr == 8) MUON_LAUNCH("norm_bwd", (norm_bwd<T, 1, 8>), grid, block, stream, a, d, parts);
   else if (s.lpr == 16) MUON_LAUNCH("norm_bwd", (norm_bwd<T, 1, 16>), grid, block, stream, a, d, parts);
