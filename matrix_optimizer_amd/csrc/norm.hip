@@ -58,10 +58,12 @@ __device__ __forceinline__ void z8(const muon_norm_args& a, const Drop& d, uint6
   }
 }
 
-// Scale of a group whose largest magnitude is `most`.
-__device__ __forceinline__ float scale_of(float most, float top) {
-  return most == 0.f ? 1.f : fmaxf(most / top, 0x1p-126f);
+// Scale of a group whose largest magnitude is `most`; `unit` = 1 / FMAX.
+__device__ __forceinline__ float scale_of(float most, float unit) {
+  return most == 0.f ? 1.f : fmaxf(most * unit, 0x1p-126f);
 }
+// 1 / FMAX of an 8-bit type.
+__device__ __forceinline__ float unit_of(int y_dtype) { return y_dtype == MUON_ROW_E5M2 ? 1.f / 57344.f : 1.f / 448.f; }
 
 // y of columns c .. c+7 at its type; an 8-bit y with the group's scale, found
 // across the group's lanes unless the row's is given.  LPR: lanes of a row if
@@ -79,11 +81,14 @@ __device__ __forceinline__ void store_y(const muon_norm_args& a, int64_t r, I c,
       float most = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(y[j]));
-      for (int o = LPR ? min(a.group / 16, LPR / 2) : a.group / 16; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, WAVE));
-      scale = scale_of(most, e5 ? 57344.f : 448.f);
+      most = fmaxf(most, dpp<0xB1>(most));
+      most = fmaxf(most, dpp<0x4E>(most));
+      if (a.group > 32) most = fmaxf(most, dpp<0x141>(most));
+      if (LPR != 8 && a.group > 64) most = fmaxf(most, dpp<0x140>(most));
+      scale = scale_of(most, unit_of(a.y_dtype));
       if (c < cols && (c & (a.group - 1)) == 0) a.scales[r * a.scales_stride + c / a.group] = scale;
     }
-    const float inv = 1.f / scale;
+    const float inv = __builtin_amdgcn_rcpf(scale);   // 2^-126 <= scale < 2^126: 1 ulp
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] *= inv;
     uint8_t* row = static_cast<uint8_t*>(a.y) + r * a.y_stride;
@@ -97,21 +102,6 @@ __device__ __forceinline__ void store_y(const muon_norm_args& a, int64_t r, I c,
 // The 8-bit scale of a whole row is one more reduction.
 __device__ __forceinline__ bool row_scaled(const muon_norm_args& a) {
   return a.y_dtype >= MUON_ROW_E4M3 && a.group == 0;
-}
-__device__ __forceinline__ float fmax_of(int y_dtype) { return y_dtype == MUON_ROW_E5M2 ? 57344.f : 448.f; }
-
-// Sum / maximum over LPR neighbouring lanes.
-template <int LPR>
-__device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-  for (int o = LPR / 2; o >= 1; o >>= 1) v += __shfl_xor(v, o, WAVE);
-  return v;
-}
-template <int LPR>
-__device__ __forceinline__ float lanes_max(float v) {
-#pragma unroll
-  for (int o = LPR / 2; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, WAVE));
-  return v;
 }
 
 // Where a lane stands: `lanes` lanes share a row, this is the t-th of them;
@@ -149,6 +139,7 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_fwd(muon_norm_args a, Dro
   int64_t r = at.r;
   uint64_t seed, offset;
   drop_seed(d, seed, offset);
+  const float per_col = 1.f / (float)cols;
   const T* x = static_cast<const T*>(a.x);
   const T* res = static_cast<const T*>(a.residual);
   float w[NC][8];
@@ -187,8 +178,8 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_fwd(muon_norm_args a, Dro
         if (res) cr[i].load(res + (r + step) * a.residual_stride, c, cols);
       }
     }
-    ss = LPR ? lanes_sum<LPR>(ss) : group_sum(ss, sums, turn);
-    const float rstd = 1.f / sqrtf(ss / (float)cols + a.eps);
+    ss = LPR ? over_row<LPR ? LPR : WAVE>(ss, add_f) : group_sum(ss, sums, turn);
+    const float rstd = 1.f / sqrtf(ss * per_col + a.eps);
     if (a.rstd && t == 0) a.rstd[r] = rstd;
     if (a.h) {
 #pragma unroll
@@ -207,8 +198,8 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_fwd(muon_norm_args a, Dro
       }
     float row_scale = 1.f;
     if (row_scaled(a)) {
-      most = LPR ? lanes_max<LPR>(most) : group_max(most, maxima, turn);
-      row_scale = scale_of(most, fmax_of(a.y_dtype));
+      most = LPR ? over_row<LPR ? LPR : WAVE>(most, max_f) : group_max(most, maxima, turn);
+      row_scale = scale_of(most, unit_of(a.y_dtype));
       if (t == 0) a.scales[r * a.scales_stride] = row_scale;
     }
 #pragma unroll
@@ -248,7 +239,7 @@ __global__ __launch_bounds__(512) void norm_fwd_long(muon_norm_args a, Drop d) {
         for (int j = 0; j < 8; ++j) most = fmaxf(most, c + j < a.cols ? fabsf(z[j] * rstd * w[j]) : 0.f);
       }
       most = group_max(most, maxima, turn);
-      row_scale = scale_of(most, fmax_of(a.y_dtype));
+      row_scale = scale_of(most, unit_of(a.y_dtype));
       if (threadIdx.x == 0) a.scales[r * a.scales_stride] = row_scale;
     }
     for (int64_t c0 = 0; c0 < a.cols; c0 += pass) {
@@ -281,6 +272,7 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_bwd(muon_norm_grad_args a
   int64_t r = at.r;
   uint64_t seed, offset;
   drop_seed(d, seed, offset);
+  const float per_col = 1.f / (float)cols;
   const T* dy = static_cast<const T*>(a.dy);
   const T* h = static_cast<const T*>(a.h);
   const T* dh = static_cast<const T*>(a.dh);
@@ -326,7 +318,7 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_bwd(muon_norm_grad_args a
       }
     }
     if (AHEAD && r + step < a.rows) fetch(r + step);
-    const float mean = (LPR ? lanes_sum<LPR>(dot) : group_sum(dot, sums, turn)) / (float)cols;
+    const float mean = (LPR ? over_row<LPR ? LPR : WAVE>(dot, add_f) : group_sum(dot, sums, turn)) * per_col;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = (i * lanes + t) * 8;

@@ -19,34 +19,6 @@ constexpr int kNone = INT32_MIN;        // the same as an ordered key
 // A row's experts over LPT lanes, NC chunks of eight to a lane: expert
 // (i LPT + t) 8 + j is element 8 i + j of the t-th lane.  64 / LPT rows a wave.
 
-// Value of another lane of the same row; every lane of the wave is active.
-template <int CTRL>
-__device__ __forceinline__ int dpp(int v) { return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true); }
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) { return (uint32_t)dpp<CTRL>((int)v); }
-template <int CTRL>
-__device__ __forceinline__ double dpp(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)(b >> 32)) << 32 | dpp<CTRL>((uint32_t)b));
-}
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) { return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(int, v))); }
-
-// f over the LPT lanes of a row, the result in each of them: two exchanges
-// within four lanes, then mirrored halves of 8 and 16 lanes, then across the
-// wave.  f is commutative, so that both sides of an exchange agree.
-template <int LPT, class V, class F>
-__device__ __forceinline__ V over_row(V v, F f) {
-  v = f(v, dpp<0xB1>(v));                              // lane ^ 1
-  v = f(v, dpp<0x4E>(v));                              // lane ^ 2
-  if constexpr (LPT >= 8) v = f(v, dpp<0x141>(v));     // lane 7 - l of eight
-  if constexpr (LPT >= 16) v = f(v, dpp<0x140>(v));    // lane 15 - l of sixteen
-  if constexpr (LPT >= 32) v = f(v, __shfl_xor(v, 16, WAVE));
-  if constexpr (LPT >= 64) v = f(v, __shfl_xor(v, 32, WAVE));
-  return v;
-}
-__device__ __forceinline__ float max_f(float a, float b) { return fmaxf(a, b); }
-__device__ __forceinline__ float add_f(float a, float b) { return a + b; }
 __device__ __forceinline__ int max_i(int a, int b) { return a > b ? a : b; }
 __device__ __forceinline__ double add_d(double a, double b) { return a + b; }
 __device__ __forceinline__ double max_d(double a, double b) { return fmax(a, b); }
@@ -85,7 +57,7 @@ __device__ __forceinline__ void route_row_64(const muon_route_spec& s, const muo
   if (soft) {
 #pragma unroll 4
     for (int e = lane; e < E; e += WAVE) top = fmaxf(top, read_logit(ld_as_f32(row, e)));
-    top = wave_max(top);
+    top = over_row<WAVE>(top, max_f);
     total = 0.0;
 #pragma unroll 1
     for (int e = lane; e < E; e += WAVE) {

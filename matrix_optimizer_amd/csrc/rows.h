@@ -114,27 +114,21 @@ __device__ __forceinline__ void store8(float* row, I c, I cols, const float* f) 
   }
 }
 
-// Limited to +-top; a NaN stays one.
-__device__ __forceinline__ float limit(float v, float top) { return v > top ? top : (v < -top ? -top : v); }
-
-// Eight values (already divided by their scale) in an 8-bit format, rounded
-// to nearest even.
+// Eight values divided by their scale in an 8-bit format, rounded to nearest
+// even.  They are at most FMAX (1 + 2^-22) in magnitude, which rounds to FMAX,
+// or NaN, which stays one: there is nothing to limit.
 template <bool E5M2, class I>
 __device__ __forceinline__ void store8_8bit(uint8_t* row, I c, I cols, const float* f) {
-  constexpr float top = E5M2 ? 57344.f : 448.f;
-  float v[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = limit(f[j], top);
   u32x2_any w;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     int p = 0;
     if constexpr (E5M2) {
-      p = __builtin_amdgcn_cvt_pk_bf8_f32(v[4 * q], v[4 * q + 1], p, false);
-      p = __builtin_amdgcn_cvt_pk_bf8_f32(v[4 * q + 2], v[4 * q + 3], p, true);
+      p = __builtin_amdgcn_cvt_pk_bf8_f32(f[4 * q], f[4 * q + 1], p, false);
+      p = __builtin_amdgcn_cvt_pk_bf8_f32(f[4 * q + 2], f[4 * q + 3], p, true);
     } else {
-      p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * q], v[4 * q + 1], p, false);
-      p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * q + 2], v[4 * q + 3], p, true);
+      p = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * q], f[4 * q + 1], p, false);
+      p = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * q + 2], f[4 * q + 3], p, true);
     }
     w[q] = (uint32_t)p;
   }
@@ -184,11 +178,34 @@ __device__ __forceinline__ void drop8(const Drop& d, uint64_t seed, uint64_t off
   }
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, WAVE));
+// Value of another lane of the same row; the row's lanes are active.
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) { return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true); }
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) { return (uint32_t)dpp<CTRL>((int)v); }
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)(b >> 32)) << 32 | dpp<CTRL>((uint32_t)b));
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) { return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(int, v))); }
+
+// f over the LPT lanes of a row, the result in each of them: two exchanges
+// within four lanes, then mirrored halves of 8 and 16 lanes, then across the
+// wave.  f is commutative, so that both sides of an exchange agree.
+template <int LPT, class V, class F>
+__device__ __forceinline__ V over_row(V v, F f) {
+  v = f(v, dpp<0xB1>(v));                              // lane ^ 1
+  v = f(v, dpp<0x4E>(v));                              // lane ^ 2
+  if constexpr (LPT >= 8) v = f(v, dpp<0x141>(v));     // lane 7 - l of eight
+  if constexpr (LPT >= 16) v = f(v, dpp<0x140>(v));    // lane 15 - l of sixteen
+  if constexpr (LPT >= 32) v = f(v, __shfl_xor(v, 16, WAVE));
+  if constexpr (LPT >= 64) v = f(v, __shfl_xor(v, 32, WAVE));
   return v;
 }
+__device__ __forceinline__ float max_f(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float add_f(float a, float b) { return a + b; }
 
 // Sum / maximum over a workgroup of up to 8 waves, in wave order.  `lds` holds
 // two sets of 8 floats, zero at first; `turn` alternates 0 and 1 from call to
@@ -203,14 +220,14 @@ __device__ __forceinline__ void red_init(GroupRed& g) {
   __syncthreads();
 }
 __device__ __forceinline__ float group_sum(float v, GroupRed& g, int turn) {
-  v = wave_sum(v);
+  v = over_row<WAVE>(v, add_f);
   if ((threadIdx.x & (WAVE - 1)) == 0) g.s[turn][threadIdx.x / WAVE] = v;
   __syncthreads();
   const f32x4 a = *reinterpret_cast<const f32x4*>(g.s[turn]), b = *reinterpret_cast<const f32x4*>(g.s[turn] + 4);
   return ((a[0] + a[1]) + (a[2] + a[3])) + ((b[0] + b[1]) + (b[2] + b[3]));
 }
 __device__ __forceinline__ float group_max(float v, GroupRed& g, int turn) {   // v >= 0
-  v = wave_max(v);
+  v = over_row<WAVE>(v, max_f);
   if ((threadIdx.x & (WAVE - 1)) == 0) g.s[turn][threadIdx.x / WAVE] = v;
   __syncthreads();
   const f32x4 a = *reinterpret_cast<const f32x4*>(g.s[turn]), b = *reinterpret_cast<const f32x4*>(g.s[turn] + 4);
