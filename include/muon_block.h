@@ -145,7 +145,8 @@ muon_status muon_norm_workspace_bytes(int64_t rows, int64_t cols, size_t* out);
  *   weight scale s, or with renormalise scale s / (sum of the chosen s),
  *          which is formed from differences of log s and so holds where every
  *          s underflows.
- * Limits: E <= 1024, top_k <= 32, top_k <= top_groups E / groups. */
+ * The bias is finite.  Limits: E <= 1024, top_k <= 32, top_k <= top_groups
+ * E / groups. */
 typedef enum { MUON_SCORE_SOFTMAX = 0, MUON_SCORE_SIGMOID = 1 } muon_score;
 #define MUON_ROUTE_MAX_EXPERTS 1024
 #define MUON_ROUTE_MAX_TOP_K 32
@@ -178,7 +179,8 @@ muon_status muon_route_forward(const muon_route_spec* spec, const muon_route_arg
  *   sigmoid: dl_e = (a_e + dscores_e s_e) (1 - s_e);
  *   softmax: dl_e = a_e - s_e sum_k a_k (zero with renormalise)
  *                   + s_e (dscores_e - sum s dscores);
- * a_e = 0 for an expert that was not chosen.  Closed experts and rows without
+ * a_e = 0 for an expert that was not chosen.  A row's experts are distinct, as
+ * the forward pass gives them; an entry outside [0, E) counts as none.  Closed experts and rows without
  * a chosen expert get 0.  The bias only moves the choice and has no gradient;
  * groups and group_top are not read. */
 typedef struct {

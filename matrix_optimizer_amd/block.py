@@ -7,7 +7,9 @@ As in binding.py: argument marshalling only, on device memory the caller owns
 hipStream_t; a missing library raises, there is no fallback.  Shapes, types
 and devices are checked here, since the C ABI sees only addresses; values,
 strides, alignment and overlap are checked there (MuonError).  Matrices are
-[rows, cols] tensors whose last dimension is contiguous; any row stride.
+[rows, cols] tensors whose last dimension is contiguous; any row stride.  With
+a stream given, the caller orders it against the tensors' own use and keeps
+them until it has run the call.
 """
 from __future__ import annotations
 

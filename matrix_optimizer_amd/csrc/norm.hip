@@ -432,26 +432,29 @@ constexpr int DWC = 32, DWL = 32;
 __global__ __launch_bounds__(DWC* DWL) void norm_dw_sum(int64_t cols, int64_t n, const float* parts, float* dw) {
   __shared__ float s[DWL][DWC + 1];
   const int cc = threadIdx.x % DWC, k = threadIdx.x / DWC;
-  const int64_t c = blockIdx.x * (int64_t)DWC + cc;
-  float v = 0.f;
-  if (c < cols) {
-    int64_t p = k;
-    for (; p + 7 * DWL < n; p += 8 * DWL) {   // eight loads in flight
-      float e[8];
+  for (int64_t c0 = blockIdx.x * (int64_t)DWC; c0 < cols; c0 += (int64_t)gridDim.x * DWC) {
+    const int64_t c = c0 + cc;
+    float v = 0.f;
+    if (c < cols) {
+      int64_t p = k;
+      for (; p + 7 * DWL < n; p += 8 * DWL) {   // eight loads in flight
+        float e[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) e[q] = parts[(p + q * DWL) * cols + c];
+        for (int q = 0; q < 8; ++q) e[q] = parts[(p + q * DWL) * cols + c];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v += e[q];
+        for (int q = 0; q < 8; ++q) v += e[q];
+      }
+      for (; p < n; p += DWL) v += parts[p * cols + c];
     }
-    for (; p < n; p += DWL) v += parts[p * cols + c];
-  }
-  s[k][cc] = v;
-  __syncthreads();
-  if (k == 0 && c < cols) {
-    v = 0.f;
+    s[k][cc] = v;
+    __syncthreads();
+    if (k == 0 && c < cols) {
+      v = 0.f;
 #pragma unroll
-    for (int q = 0; q < DWL; ++q) v += s[q][cc];
-    dw[c] = v;
+      for (int q = 0; q < DWL; ++q) v += s[q][cc];
+      dw[c] = v;
+    }
+    __syncthreads();
   }
 }
 
@@ -497,14 +500,16 @@ int64_t resident(const RowShape& s) { return 256 * (s.nc == 1 ? (1024 + s.thread
 }  // namespace
 
 // Backward: each workgroup leaves a row of partial sums, written and read
-// again.  Two workgroups a CU where a lane keeps one chunk ([16384, 4096] with
-// dropout: 110 us, one 117, four 124), one where it keeps more ([4096, 8192]:
-// 43 us, two 48) and where two would leave fewer than 8 rows to each; up to 4
-// rows in a row a single one, which needs no second launch.
+// again, which costs as much as parts / rows of the whole.  As many as keep
+// the memory busy, 1024 lanes a CU ([12010, 1728] bf16: 39 us, 53 by half), as
+// long as each has 12 rows; one a CU where a lane keeps more chunks ([4096,
+// 8192]: 43 us, two 48); up to 4 rows in a row a single one, which needs no
+// second launch.
 int64_t norm_parts(int64_t rows, int64_t cols) {
   const RowShape s = row_shape(cols);
   const int64_t groups = (rows + s.per_group - 1) / s.per_group;
-  return groups <= 4 ? std::min<int64_t>(groups, 1) : even(groups, s.nc == 1 && groups >= 4096 ? 512 : 256);
+  if (groups <= 4) return std::min<int64_t>(groups, 1);
+  return even(groups, s.nc == 1 ? std::min(resident(s), std::max<int64_t>(256, rows / 12)) : 256);
 }
 
 hipError_t run_dropout(int64_t rows, int64_t cols, const void* x, int64_t xs, void* y, int64_t ys, int dtype,
@@ -568,7 +573,7 @@ hipError_t run_norm_backward(const muon_norm_grad_args& a, const Drop& d, float*
   }
   const int64_t n = norm_parts(a.rows, a.cols);
   if (a.dweight && n != 1)   // n = 0: zeros
-    MUON_LAUNCH("norm_dw_sum", norm_dw_sum, dim3((unsigned)((a.cols + DWC - 1) / DWC)), dim3(DWC * DWL), stream, a.cols, n,
+    MUON_LAUNCH("norm_dw_sum", norm_dw_sum, dim3((unsigned)std::min<int64_t>((a.cols + DWC - 1) / DWC, kMaxGrid)), dim3(DWC * DWL), stream, a.cols, n,
                 parts, a.dweight);
   return hipGetLastError();
 }

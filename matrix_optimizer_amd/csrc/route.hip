@@ -158,7 +158,7 @@ __device__ __forceinline__ void route_row_64(const muon_route_spec& s, const muo
   wave_sync();
 }
 
-// A chosen expert's score: exp(l - top), the difference's rounding made good,
+// A score: exp(l - top), the difference's rounding made good,
 // or sigmoid(l) without loss at either end.
 __device__ __forceinline__ float slot_score(float l, float top, bool soft) {
   if (soft) {
@@ -274,8 +274,7 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
       z = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float d = l[i] - top;
-        v[i] = !(l[i] > -HUGE_VALF) ? 0.f : fine ? expf(d) : __expf(d);
+        v[i] = !(l[i] > -HUGE_VALF) ? 0.f : fine ? slot_score(l[i], top, true) : __expf(l[i] - top);
         z += v[i];
       }
       z = over_row<LPT>(z, add_f);
@@ -625,7 +624,7 @@ __global__ __launch_bounds__(RT) void route_bwd(muon_route_spec s, muon_route_gr
       float p[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        p[i] = l[i] > -HUGE_VALF ? expf(l[i] - top) : 0.f;
+        p[i] = l[i] > -HUGE_VALF ? slot_score(l[i], top, true) : 0.f;
         z += p[i];
       }
       z = over_row<LPT>(z, add_f);

@@ -212,7 +212,7 @@ __device__ __forceinline__ float add_f(float a, float b) { return a + b; }
 // call on the same set, so that one barrier a call is enough: a wave that
 // writes a set again has passed the barrier of the call in between, and with
 // it every wave its reads of that set.
-struct GroupRed {
+struct alignas(16) GroupRed {
   float s[2][8];
 };
 __device__ __forceinline__ void red_init(GroupRed& g) {

@@ -143,6 +143,26 @@ def test_route_masks_and_extremes(score, groups, renorm):
     check(l.bfloat16(), K.Route(k, score, groups, groups, renormalise=renorm), None, mask.bool())
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e", [30, 64, 256, 1024])
+def test_route_wide_values(score, e):
+    """Logits and biases spread far wider than their usual range, the chosen ones far below the largest too."""
+    rng = np.random.default_rng(e)
+    for scale in (40.0, 1e4, 1e30):
+        l = logits_of(rng, 25, e, "f32", scale)
+        check(l, K.Route(7, score))
+        check(l, K.Route(7, score, 2, 1))
+    l = torch.zeros(9, e, device="cuda")
+    l[:, ::3] = torch.arange(l[:, ::3].shape[1], device="cuda") * -7.0 - 100.0
+    l[:, 1::3] = float("-inf")
+    l[3:, 2::3] = -3e4
+    check(l, K.Route(10, score))
+    for wide in (3.0, 1e6):
+        bias = torch.from_numpy((rng.standard_normal(e) * wide).astype(np.float32)).cuda()
+        check(logits_of(rng, 25, e, "f32"), K.Route(7, score), bias)
+        check(logits_of(rng, 25, e, "bf16"), K.Route(7, score, 2, 1), bias)
+
+
 # ---- backward ---------------------------------------------------------------
 def check_backward(logits, route, idx, w, dscores=False, rng=None, pad=0, shift=0):
     t, e = logits.shape
