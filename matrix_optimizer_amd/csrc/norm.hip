@@ -3,7 +3,8 @@
 //   z = r + D(x);  rstd = 1 / sqrt(mean(z^2) + eps);  y = z rstd w
 //   dz = rstd (g - xh mean(g xh)) + dh,  g = dy w,  xh = h rstd;  dw = sum dy xh
 //
-// All of it is bound by memory: a few operations per element.
+// All of it is bound by memory: a few operations per element, one pass over
+// each input and output.  A copy of 1 GiB reaches 5.1 TB/s on this card.
 #include <algorithm>
 
 #include "internal.h"
@@ -15,7 +16,9 @@ namespace {
 constexpr int NT = 256;            // threads of a workgroup
 constexpr int64_t kMaxGrid = 1 << 16;
 
-// D(x) alone: eight columns a lane.  `per_row` = chunks of eight in a row.
+// D(x) alone: eight columns a lane, which share one Philox block, 16 bits an
+// element.  [8192, 28672] bf16: 163 us, 5.8 TB/s, the vector units busy 70 % of
+// it with one block; 32 bits an element would need two.
 template <typename T>
 __global__ __launch_bounds__(NT) void dropout_k(int64_t rows, int64_t cols, const T* x, int64_t xs, T* y, int64_t ys,
                                                 Drop d) {
@@ -124,7 +127,10 @@ struct RowLanes {
 // barriers up to 1024 columns, else (LPR = 0) a workgroup of up to 512 lanes a
 // row.  The workgroups stay and step over the rows; the next row's loads are
 // issued before this row's reduction and stores, so that memory is busy
-// meanwhile.
+// meanwhile.  Measured: [16384, 4096] bf16 with residual and p = 0.1 102 us,
+// 5.3 TB/s (two passes over the row 135); [4096, 8192] to e4m3 with a scale per
+// 128 columns 45 us, 5.2 TB/s; [65536, 128] 13 us; one row of 4096 3.4 us, less
+// than the call.
 template <typename T, int NC, int LPR>
 __global__ __launch_bounds__(LPR ? NT : 512) void norm_fwd(muon_norm_args a, Drop d) {
   __shared__ GroupRed sums, maxima;
@@ -260,7 +266,11 @@ __global__ __launch_bounds__(512) void norm_fwd_long(muon_norm_args a, Drop d) {
 
 // Backward, the row in registers as in norm_fwd.  dweight's sums stay in the
 // lanes' registers over all of a workgroup's rows; each workgroup leaves one
-// row of partial sums (or the result, if it is the only one).
+// row of partial sums (or the result, if it is the only one).  [16384, 4096]
+// bf16 with dropout and dh: 126 us and 5 for norm_dw_sum, 5.1 TB/s of the
+// bytes without the partial sums (passes of their own for dz and dweight 346);
+// [777, 2051] fp32 in a wider buffer 10 + 4 us, the latency of four rows in a
+// row and of two launches.
 template <typename T, int NC, int LPR>
 __global__ __launch_bounds__(LPR ? NT : 512) void norm_bwd(muon_norm_grad_args a, Drop d, float* parts) {
   __shared__ GroupRed sums;
@@ -491,10 +501,10 @@ int64_t even(int64_t groups, int64_t most) {
 
 // Forward: workgroups that stay on the GPU, at least 1024 lanes on each of 256
 // CUs where a lane keeps one chunk, two workgroups where it keeps more.
-// [16384, 4096] bf16 with p = 0.1: 105 us, 111 with twice as many (the last
-// round of workgroups is then part empty), 111 with half; [3777, 2880] by
-// three workgroups of 384 lanes 20 us, by two or four 24 (a fourth does not fit
-// the SIMD that holds two waves of each).
+// [16384, 4096] bf16 with p = 0.1: half as many 6 % slower, twice as many 3 %
+// (the last round of workgroups is then part empty); [3777, 2880] by three
+// workgroups of 384 lanes 20 us, by two or four 24 (a fourth does not fit the
+// SIMD that holds two waves of each).
 int64_t resident(const RowShape& s) { return 256 * (s.nc == 1 ? (1024 + s.threads - 1) / s.threads : 1024 / s.threads); }
 
 }  // namespace
