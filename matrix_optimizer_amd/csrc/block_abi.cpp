@@ -273,8 +273,8 @@ muon_status muon_route_order(int64_t num_pairs, int64_t num_experts, const int32
   Buffers b;
   b.flat(counts, num_experts, 4, true);
   b.flat(offsets, num_experts + 1, 4, true);
-  b.flat(workspace, int64_t(need), 1, true, 256);
   if (num_pairs > 0) {
+    b.flat(workspace, int64_t(need), 1, true, 256);
     b.flat(experts, num_pairs, 4, false);
     b.flat(order, num_pairs, 4, true);
     b.flat(position, num_pairs, 4, true);

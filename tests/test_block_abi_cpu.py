@@ -193,6 +193,10 @@ def test_order_and_balance_refusals(mem):
     assert order(o=mem(1) + 60) == order(d=mem(0)) == INVALID
     assert order(wb=need - 1) == SMALL
     assert order(n=(1 << 31) - 1) == order(e=1025) == UNSUPPORTED
+    # no pairs: no workspace, and nothing but counts and offsets (the launch fails here, there is no device)
+    assert K.route_order_workspace_bytes(0, 16) == 0
+    assert order(n=0, x=None, d=None, p=None, w=None, wb=0) == B.MUON_ERR_HIP
+    assert order(n=0, c=None) == INVALID
     bal = lambda n=16, c=mem(0), b=mem(1), o=mem(2), r=0.1: L.muon_route_balance(n, c, b, o, r, None)  # noqa: E731
     assert bal(n=0) == bal(c=None) == bal(b=None) == bal(o=None) == bal(r=float("nan")) == bal(o=mem(0)) == INVALID
     assert bal(o=mem(1) + 4) == INVALID

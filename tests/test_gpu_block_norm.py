@@ -177,6 +177,19 @@ def test_norm_forward_tiny_scale():
     close(f64(y), np.full((1, 64), float(w[0]) / 2.0 ** -126), "e4m3", 1e-37 / 2.0 ** -126, 64, "y")
 
 
+EDGES = [63, 65, 127, 128, 255, 257, 511, 512, 513, 1023, 1024, 1025, 4095, 4097, 8192, 8193, 16383, 16385]
+
+
+@pytest.mark.parametrize("c", EDGES)
+def test_norm_widths_where_the_layout_changes(c):
+    """Widths beside those at which a row goes to more lanes, to a workgroup, to more chunks a lane, to passes."""
+    for r in (1, 5, 70):
+        run_forward(np.random.default_rng(c), r, c, "bf16", "e4m3", 128, drop=(0.1, 1, c))
+        run_forward(np.random.default_rng(c), r, c, "f32", "bf16", weight="bf16")
+        run_backward(np.random.default_rng(c), r, c, "bf16", drop=(0.1, 1, c))
+        run_backward(np.random.default_rng(c), r, c, "f32", stream=False)
+
+
 def run_backward(rng, r, c, kind, weight="f32", stream=True, drop=None, pad=0, shift=0, dx=True, dr=True, inplace=False):
     h, dy = rows(rng, r, c, kind, 2.0, pad, shift), rows(rng, r, c, kind, 0.1, pad, shift)
     dh = rows(rng, r, c, kind, 0.1, pad, shift) if stream else None
