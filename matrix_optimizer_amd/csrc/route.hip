@@ -317,6 +317,8 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
     }
   }
   bool unsure = false;   // grade 3
+  bool out[NC] = {};     // whole chunks whose group does not stay
+  bool single = shut;    // some v are -inf
   if (G > 1) {
     float* by_l = wave_lds + (size_t)(lane / LPT) * (E + 2 * G);
     float* of_l = by_l + E;
@@ -389,11 +391,10 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int g = (i * LPT + t) / span;
-        const bool out = g < G && !in_l[g];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[8 * i + j] = out ? -HUGE_VALF : v[8 * i + j];
+        out[i] = g < G && !in_l[g];
       }
     } else {
+      single = true;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int e = ((i / 8) * LPT + t) * 8 + i % 8;
@@ -430,16 +431,21 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
       const float by = a.bias ? 0x1p20f : 0x1p17f;
       if (a.bias) apart = (int)fminf(2.f + by * (tol + 0x1p-22f * (fabsf(most) + 2.f)), 0x1p22f);
 #pragma unroll
-      for (int i = 0; i < V; ++i) num[i] = (int)fmaxf((v[i] - most) * by, (float)kLow) * (kIndex + 1);
+      for (int i = 0; i < V; ++i)   // v - most in steps, rounded once; never above 0
+        num[i] = (int)__builtin_amdgcn_fmed3f(__builtin_fmaf(v[i], by, -most * by), (float)kLow, 0.f) * (kIndex + 1);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       constexpr int upper = kIndex & ~(LPT * 8 - 1);
       num[i] = num[i] | low | ((upper - (i / 8) * LPT * 8) + (7 - i % 8));
     }
-    if (shut || G > 1) {
+    if (single) {
 #pragma unroll
       for (int i = 0; i < V; ++i) num[i] = v[i] > -HUGE_VALF ? num[i] : kNone;
+    }
+    if (G > 1) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) num[i] = out[i / 8] ? kNone : num[i];
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) m = max_i(m, num[i]);
