@@ -25,12 +25,14 @@ __global__ __launch_bounds__(NT) void dropout_k(int64_t rows, int64_t cols, cons
   uint64_t seed, offset;
   drop_seed(d, seed, offset);
   const int64_t per_row = (cols + 7) / 8, total = rows * per_row;
+  const uint32_t n = (uint32_t)cols;   // below 2^31
   for (int64_t i = blockIdx.x * (int64_t)NT + threadIdx.x; i < total; i += (int64_t)gridDim.x * NT) {
-    const int64_t r = i / per_row, c = (i - r * per_row) * 8;
+    const int64_t r = total <= UINT32_MAX ? (uint32_t)i / (uint32_t)per_row : i / per_row;
+    const uint32_t c = (uint32_t)(i - r * per_row) * 8;
     float f[8];
-    load8(x + r * xs, c, cols, f);
+    load8(x + r * xs, c, n, f);
     if (d.on) drop8(d, seed, offset, r, c, f);
-    store8(y + r * ys, c, cols, f);
+    store8(y + r * ys, c, n, f);
   }
 }
 
@@ -165,11 +167,11 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_fwd(muon_norm_args a, Dro
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = (i * lanes + t) * 8;
-      cx[i].get(z[i]);
+      cx[i].get(z[i], c, cols);
       if (d.on) drop8(d, seed, offset, r, c, z[i]);
       if (res) {
         float e[8];
-        cr[i].get(e);
+        cr[i].get(e, c, cols);
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[i][j] += e[j];
       }
@@ -316,8 +318,9 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_bwd(muon_norm_grad_args a
     const float rs = rstd;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      cg[i].get(g[i]);
-      ch[i].get(xh[i]);
+      const int c = (i * lanes + t) * 8;
+      cg[i].get(g[i], c, cols);
+      ch[i].get(xh[i], c, cols);
       e[i] = cd[i];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -337,7 +340,7 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_bwd(muon_norm_grad_args a
       for (int j = 0; j < 8; ++j) g[i][j] = rs * (g[i][j] - xh[i][j] * mean);
       if (dh) {
         float f[8];
-        e[i].get(f);
+        e[i].get(f, c, cols);
 #pragma unroll
         for (int j = 0; j < 8; ++j) g[i][j] += f[j];
       }

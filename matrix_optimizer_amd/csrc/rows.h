@@ -22,46 +22,86 @@ __device__ __forceinline__ void unpack8(const u32x4& v, float* f) {
 
 // Columns c .. c+7 of a row in their stored form, zeros from column `cols` on
 // (c may lie past it): 4 registers of bf16 or 8 of fp32, so that loads can be
-// in flight while the row before is worked on.  Lanes past the row's end skip
-// the loads of single columns, which only the row's last chunk needs.
+// in flight while the row before is worked on.  The row's last chunk is the
+// row's last eight columns, moved down by get() and not before, since that
+// waits for them ([16384, 4095] bf16: norm forward and backward 123 and 96 us,
+// 191 and 161 with a load for each column behind its own test).
+typedef uint16_t u16_any __attribute__((aligned(1)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
+
 template <typename T> struct Chunk;
 template <> struct Chunk<bf16_t> {
   u32x4 v;
+  // elements n .. 7 to 0 .., zeros after them; n in 1 .. 7
+  __device__ __forceinline__ void down(int n) {
+    uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+    lo = n & 4 ? hi : lo;
+    hi = n & 4 ? 0 : hi;
+    const int s = (n & 3) * 16;
+    lo = lo >> s | (hi << 1) << (63 - s);
+    hi >>= s;
+    v = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+  }
   template <class I>
   __device__ __forceinline__ void load(const bf16_t* row, I c, I cols) {
-    if (c + 8 <= cols) {
-      v = *reinterpret_cast<const u32x4_any*>(row + c);
-    } else if (c >= cols) {
+    if (cols >= 8) {   // one load for full chunks and the last
       v = u32x4{};
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t lo = c + 2 * q < cols ? row[c + 2 * q] : 0, hi = c + 2 * q + 1 < cols ? row[c + 2 * q + 1] : 0;
-        v[q] = lo | (hi << 16);
-      }
+      if (c < cols) v = *reinterpret_cast<const u32x4_any*>(row + (c + 8 <= cols ? c : cols - 8));
+    } else {   // the whole row, its last element first
+      v = u32x4{};
+      if (c > 0) return;
+#pragma unroll 1
+      for (int j = (int)cols - 1; j >= 0; --j)
+        v = u32x4{v[0] << 16 | row[j], v[1] << 16 | v[0] >> 16, v[2] << 16 | v[1] >> 16, v[3] << 16 | v[2] >> 16};
     }
   }
-  __device__ __forceinline__ void get(float* f) const { unpack8(v, f); }
+  template <class I>
+  __device__ __forceinline__ void get(float* f, I c, I cols) {
+    if (c < cols && c + 8 > cols && cols >= 8) down((int)(c + 8 - cols));
+    unpack8(v, f);
+  }
 };
 template <> struct Chunk<float> {
   u32x4 a, b;
+  __device__ __forceinline__ void down(int n) {
+    const u32x4 z = {};
+    if (n & 4) {
+      a = b;
+      b = z;
+    }
+    if (n & 2) {
+      a = u32x4{a[2], a[3], b[0], b[1]};
+      b = u32x4{b[2], b[3], 0, 0};
+    }
+    if (n & 1) {
+      a = u32x4{a[1], a[2], a[3], b[0]};
+      b = u32x4{b[1], b[2], b[3], 0};
+    }
+  }
   template <class I>
   __device__ __forceinline__ void load(const float* row, I c, I cols) {
-    if (c + 8 <= cols) {
-      a = *reinterpret_cast<const u32x4_any*>(row + c);
-      b = *reinterpret_cast<const u32x4_any*>(row + c + 4);
-    } else if (c >= cols) {
+    if (cols >= 8) {
       a = u32x4{};
       b = u32x4{};
+      if (c < cols) {
+        const float* p = row + (c + 8 <= cols ? c : cols - 8);
+        a = *reinterpret_cast<const u32x4_any*>(p);
+        b = *reinterpret_cast<const u32x4_any*>(p + 4);
+      }
     } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        a[j] = c + j < cols ? __float_as_uint(row[c + j]) : 0;
-        b[j] = c + j + 4 < cols ? __float_as_uint(row[c + j + 4]) : 0;
+      a = u32x4{};
+      b = u32x4{};
+      if (c > 0) return;
+#pragma unroll 1
+      for (int j = (int)cols - 1; j >= 0; --j) {
+        b = u32x4{a[3], b[0], b[1], b[2]};
+        a = u32x4{__float_as_uint(row[j]), a[0], a[1], a[2]};
       }
     }
   }
-  __device__ __forceinline__ void get(float* f) const {
+  template <class I>
+  __device__ __forceinline__ void get(float* f, I c, I cols) {
+    if (c < cols && c + 8 > cols && cols >= 8) down((int)(c + 8 - cols));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       f[j] = __uint_as_float(a[j]);
@@ -74,42 +114,64 @@ template <typename T, class I>
 __device__ __forceinline__ void load8(const T* row, I c, I cols, float* f) {
   Chunk<T> k;
   k.load(row, c, cols);
-  k.get(f);
+  k.get(f, c, cols);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return (uint32_t)f2bf(lo) | ((uint32_t)f2bf(hi) << 16);
 }
 
-// The same columns rounded and stored; those from `cols` on are left alone.
+// The same columns rounded and stored; those from `cols` on are left alone (the
+// row's last chunk goes by pieces of 4, 2 and 1).
 template <class I>
 __device__ __forceinline__ void store8(bf16_t* row, I c, I cols, const float* f) {
+  u32x4 v;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = pack_bf16(f[2 * q], f[2 * q + 1]);
   if (c + 8 <= cols) {
-    u32x4 v;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = pack_bf16(f[2 * q], f[2 * q + 1]);
     *reinterpret_cast<u32x4_any*>(row + c) = v;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j < cols) row[c + j] = f2bf(f[j]);
+  } else if (c < cols) {
+    const int n = (int)(cols - c);
+    bf16_t* p = row + c;
+    if (n & 4) {
+      *reinterpret_cast<u32x2_any*>(p) = u32x2_any{v[0], v[1]};
+      v[0] = v[2];
+      v[1] = v[3];
+      p += 4;
+    }
+    if (n & 2) {
+      *reinterpret_cast<u32_any*>(p) = v[0];
+      v[0] = v[1];
+      p += 2;
+    }
+    if (n & 1) *p = (bf16_t)v[0];
   }
 }
 template <class I>
 __device__ __forceinline__ void store8(float* row, I c, I cols, const float* f) {
-  if (c + 8 <= cols) {
-    u32x4 a, b;
+  u32x4 a, b;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      a[j] = __float_as_uint(f[j]);
-      b[j] = __float_as_uint(f[j + 4]);
-    }
+  for (int j = 0; j < 4; ++j) {
+    a[j] = __float_as_uint(f[j]);
+    b[j] = __float_as_uint(f[j + 4]);
+  }
+  if (c + 8 <= cols) {
     *reinterpret_cast<u32x4_any*>(row + c) = a;
     *reinterpret_cast<u32x4_any*>(row + c + 4) = b;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j < cols) row[c + j] = f[j];
+  } else if (c < cols) {
+    const int n = (int)(cols - c);
+    float* p = row + c;
+    if (n & 4) {
+      *reinterpret_cast<u32x4_any*>(p) = a;
+      a = b;
+      p += 4;
+    }
+    if (n & 2) {
+      *reinterpret_cast<u32x2_any*>(p) = u32x2_any{a[0], a[1]};
+      a[0] = a[2];
+      p += 2;
+    }
+    if (n & 1) *p = __uint_as_float(a[0]);
   }
 }
 
@@ -133,10 +195,21 @@ __device__ __forceinline__ void store8_8bit(uint8_t* row, I c, I cols, const flo
   }
   if (c + 8 <= cols) {
     *reinterpret_cast<u32x2_any*>(row + c) = w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j < cols) row[c + j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
+  } else if (c < cols) {
+    const int n = (int)(cols - c);
+    uint8_t* p = row + c;
+    uint32_t x = w[0];
+    if (n & 4) {
+      *reinterpret_cast<u32_any*>(p) = x;
+      x = w[1];
+      p += 4;
+    }
+    if (n & 2) {
+      *reinterpret_cast<u16_any*>(p) = (uint16_t)x;
+      x >>= 16;
+      p += 2;
+    }
+    if (n & 1) *p = (uint8_t)x;
   }
 }
 
