@@ -18,8 +18,10 @@ constexpr int64_t kMaxGrid = 1 << 16;
 
 // D(x) alone: eight columns a lane, which share one Philox block, 16 bits an
 // element.  [8192, 28672] bf16: 163 us, 5.8 TB/s, the vector units busy 70 % of
-// it with one block; 32 bits an element would need two.
-template <typename T>
+// it with one block; 32 bits an element would need two.  WHOLE: a width of
+// whole chunks, which spares the tests for the last one ([16384, 4096] bf16
+// 49 us, 52 with them).
+template <typename T, bool WHOLE>
 __global__ __launch_bounds__(NT) void dropout_k(int64_t rows, int64_t cols, const T* x, int64_t xs, T* y, int64_t ys,
                                                 Drop d) {
   uint64_t seed, offset;
@@ -28,11 +30,11 @@ __global__ __launch_bounds__(NT) void dropout_k(int64_t rows, int64_t cols, cons
   const uint32_t n = (uint32_t)cols;   // below 2^31
   for (int64_t i = blockIdx.x * (int64_t)NT + threadIdx.x; i < total; i += (int64_t)gridDim.x * NT) {
     const int64_t r = total <= UINT32_MAX ? (uint32_t)i / (uint32_t)per_row : i / per_row;
-    const uint32_t c = (uint32_t)(i - r * per_row) * 8;
+    const uint32_t c = (uint32_t)(i - r * per_row) * 8, end = WHOLE ? c + 8 : n;
     float f[8];
-    load8(x + r * xs, c, n, f);
+    load8(x + r * xs, c, end, f);
     if (d.on) drop8(d, seed, offset, r, c, f);
-    store8(y + r * ys, c, n, f);
+    store8(y + r * ys, c, end, f);
   }
 }
 
@@ -525,16 +527,21 @@ int64_t norm_parts(int64_t rows, int64_t cols) {
   return even(groups, s.nc == 1 ? std::min(resident(s), std::max<int64_t>(256, rows / 12)) : 256);
 }
 
-hipError_t run_dropout(int64_t rows, int64_t cols, const void* x, int64_t xs, void* y, int64_t ys, int dtype,
-                       const Drop& d, hipStream_t stream) {
+template <typename T>
+static void launch_dropout(int64_t rows, int64_t cols, const void* x, int64_t xs, void* y, int64_t ys, const Drop& d,
+                           hipStream_t stream) {
   const int64_t chunks = rows * ((cols + 7) / 8);
   const dim3 grid((unsigned)std::min<int64_t>((chunks + NT - 1) / NT, kMaxGrid));
-  if (dtype == MUON_BF16)
-    MUON_LAUNCH("dropout", dropout_k<bf16_t>, grid, dim3(NT), stream, rows, cols, static_cast<const bf16_t*>(x), xs,
-                static_cast<bf16_t*>(y), ys, d);
-  else
-    MUON_LAUNCH("dropout", dropout_k<float>, grid, dim3(NT), stream, rows, cols, static_cast<const float*>(x), xs,
-                static_cast<float*>(y), ys, d);
+  const T* in = static_cast<const T*>(x);
+  T* out = static_cast<T*>(y);
+  if (cols % 8 == 0) MUON_LAUNCH("dropout", (dropout_k<T, true>), grid, dim3(NT), stream, rows, cols, in, xs, out, ys, d);
+  else MUON_LAUNCH("dropout", (dropout_k<T, false>), grid, dim3(NT), stream, rows, cols, in, xs, out, ys, d);
+}
+
+hipError_t run_dropout(int64_t rows, int64_t cols, const void* x, int64_t xs, void* y, int64_t ys, int dtype,
+                       const Drop& d, hipStream_t stream) {
+  if (dtype == MUON_BF16) launch_dropout<bf16_t>(rows, cols, x, xs, y, ys, d, stream);
+  else launch_dropout<float>(rows, cols, x, xs, y, ys, d, stream);
   return hipGetLastError();
 }
 
