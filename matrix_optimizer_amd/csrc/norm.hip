@@ -17,7 +17,7 @@ constexpr int NT = 256;            // threads of a workgroup
 constexpr int64_t kMaxGrid = 1 << 16;
 
 // D(x) alone: eight columns a lane, which share one Philox block, 16 bits an
-// element.  [8192, 28672] bf16: 163 us, 5.8 TB/s, the vector units busy 70 % of
+// element.  [8192, 28672] bf16: 163 us, 5.8 TB/s, the vector units busy 74 % of
 // it with one block; 32 bits an element would need two.  WHOLE: a width of
 // whole chunks, which spares the tests for the last one ([16384, 4096] bf16
 // 49 us, 52 with them).
@@ -131,9 +131,9 @@ struct RowLanes {
 // barriers up to 1024 columns, else (LPR = 0) a workgroup of up to 512 lanes a
 // row.  The workgroups stay and step over the rows; the next row's loads are
 // issued before this row's reduction and stores, so that memory is busy
-// meanwhile.  Measured: [16384, 4096] bf16 with residual and p = 0.1 102 us,
-// 5.3 TB/s (two passes over the row 135); [4096, 8192] to e4m3 with a scale per
-// 128 columns 45 us, 5.2 TB/s; [65536, 128] 13 us; one row of 4096 3.4 us, less
+// meanwhile.  Measured: [16384, 4096] bf16 with residual and p = 0.1 98 us,
+// 5.5 TB/s (two passes over the row 135); [4096, 8192] to e4m3 with a scale per
+// 128 columns 45 us, 5.2 TB/s; [65536, 128] 13 us; one row of 4096 3.2 us, less
 // than the call.
 template <typename T, int NC, int LPR>
 __global__ __launch_bounds__(LPR ? NT : 512) void norm_fwd(muon_norm_args a, Drop d) {

@@ -213,8 +213,8 @@ __host__ __device__ constexpr int route_wave_words(int E, int G, int rows, int c
 //
 // The choice is defined on scores in 64 bits; forming and sorting them so took
 // 275 us for 32768 rows of 256 experts in 8 groups, of which the bytes are 4;
-// now 20 us (15 without groups, 10 without bias), 14 of them vector
-// instructions, 1020 a wave.
+// now 21 us (15 without groups, 10 without bias), 14 of them vector
+// instructions, 1030 a wave.
 // What bounds it is the instructions of the choice, and at the end the longest
 // wave, so a row gets 4 to 64 lanes (16 for 256 experts, four rows a wave),
 // and the choice is made in three grades, each for the rows that the one
