@@ -65,12 +65,11 @@ __device__ __forceinline__ void z8(const muon_norm_args& a, const Drop& d, uint6
   }
 }
 
-// Scale of a group whose largest magnitude is `most`; `unit` = 1 / FMAX.
-__device__ __forceinline__ float scale_of(float most, float unit) {
+// Scale of a group whose largest magnitude is `most`.
+__device__ __forceinline__ float scale_of(float most, int y_dtype) {
+  const float unit = y_dtype == MUON_ROW_E5M2 ? 1.f / 57344.f : 1.f / 448.f;
   return most == 0.f ? 1.f : fmaxf(most * unit, 0x1p-126f);
 }
-// 1 / FMAX of an 8-bit type.
-__device__ __forceinline__ float unit_of(int y_dtype) { return y_dtype == MUON_ROW_E5M2 ? 1.f / 57344.f : 1.f / 448.f; }
 
 // y of columns c .. c+7 at its type; an 8-bit y with the group's scale, found
 // across the group's lanes unless the row's is given.  LPR: lanes of a row if
@@ -92,12 +91,20 @@ __device__ __forceinline__ void store_y(const muon_norm_args& a, int64_t r, I c,
       most = fmaxf(most, dpp<0x4E>(most));
       if (a.group > 32) most = fmaxf(most, dpp<0x141>(most));
       if (LPR != 8 && a.group > 64) most = fmaxf(most, dpp<0x140>(most));
-      scale = scale_of(most, unit_of(a.y_dtype));
+      scale = scale_of(most, a.y_dtype);
       if (c < cols && (c & (a.group - 1)) == 0) a.scales[r * a.scales_stride + c / a.group] = scale;
     }
-    const float inv = __builtin_amdgcn_rcpf(scale);   // 2^-126 <= scale < 2^126: 1 ulp
+    // y / scale as fp32 divides (but for one in a million, an ulp off): 1 / scale
+    // in two floats, the first a little too small so that the second is positive
+    // and -0 keeps its sign.  2^-126 <= scale < 2^120, or infinite: then finite
+    // elements become 0 and infinite ones NaN.  One multiplication more an
+    // element than by the reciprocal alone, which moves a few in a million by an
+    // 8-bit step: [4096, 8192] 45.6 us against 45.4, [32768, 1024] by groups of 32
+    // 24.2 against 23.6.
+    const float inv = __builtin_amdgcn_rcpf(scale) * (1.f - 0x1p-22f);
+    const float rest = scale < HUGE_VALF ? __builtin_fmaf(-scale, inv, 1.f) * inv : 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] *= inv;
+    for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(y[j], inv, y[j] * rest);
     uint8_t* row = static_cast<uint8_t*>(a.y) + r * a.y_stride;
     if (c < cols) {
       if (e5) store8_8bit<true>(row, c, cols, y);
@@ -133,7 +140,7 @@ struct RowLanes {
 // issued before this row's reduction and stores, so that memory is busy
 // meanwhile.  Measured: [16384, 4096] bf16 with residual and p = 0.1 98 us,
 // 5.5 TB/s (two passes over the row 135); [4096, 8192] to e4m3 with a scale per
-// 128 columns 45 us, 5.2 TB/s; [65536, 128] 13 us; one row of 4096 3.2 us, less
+// 128 columns 45.6 us, 5.2 TB/s; [65536, 128] 13 us; one row of 4096 3.2 us, less
 // than the call.
 template <typename T, int NC, int LPR>
 __global__ __launch_bounds__(LPR ? NT : 512) void norm_fwd(muon_norm_args a, Drop d) {
@@ -209,7 +216,7 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_fwd(muon_norm_args a, Dro
     float row_scale = 1.f;
     if (row_scaled(a)) {
       most = LPR ? over_row<LPR ? LPR : WAVE>(most, max_f) : group_max(most, maxima, turn);
-      row_scale = scale_of(most, unit_of(a.y_dtype));
+      row_scale = scale_of(most, a.y_dtype);
       if (t == 0) a.scales[r * a.scales_stride] = row_scale;
     }
 #pragma unroll
@@ -249,7 +256,7 @@ __global__ __launch_bounds__(512) void norm_fwd_long(muon_norm_args a, Drop d) {
         for (int j = 0; j < 8; ++j) most = fmaxf(most, c + j < a.cols ? fabsf(z[j] * rstd * w[j]) : 0.f);
       }
       most = group_max(most, maxima, turn);
-      row_scale = scale_of(most, unit_of(a.y_dtype));
+      row_scale = scale_of(most, a.y_dtype);
       if (threadIdx.x == 0) a.scales[r * a.scales_stride] = row_scale;
     }
     for (int64_t c0 = 0; c0 < a.cols; c0 += pass) {

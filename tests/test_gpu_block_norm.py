@@ -415,3 +415,46 @@ def test_graph_replays_with_device_seed():
         step(K.Dropout(0.2, 100 + k, k << 40))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, (h, y, rstd, dx, dw))), k
+
+
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("ykind", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("r,c", [(60000, 64), (4000, 1024), (1000, 4096), (200, 20000), (5001, 777)])
+def test_norm_8bit_is_the_rounded_quotient(r, c, ykind, group):
+    """The scale is max |y| times 1 / FMAX and the stored value y / scale as fp32 divides, rounded to 8 bits:
+    equal bit for bit to the fp32 output of the same call divided on the host."""
+    rng = np.random.default_rng(r + group)
+    x, res = rows(rng, r, c, "bf16"), rows(rng, r, c, "bf16", 2.0)
+    x[0, :16], res[0, :16] = -0.0, -0.0
+    w = rows(rng, 1, c, "f32", 0.2).reshape(-1) + 1
+    y, q = torch.empty(r, c, device="cuda"), torch.empty(r, c, device="cuda", dtype=T[ykind])
+    g = group or c
+    n = -(-c // g)
+    s = torch.empty(r, n, device="cuda")
+    K.muon_norm_forward(x, y, residual=res, weight=w, eps=EPS)
+    K.muon_norm_forward(x, q, residual=res, weight=w, scales=s, group=group, eps=EPS)
+    y, q, s = y.cpu(), q.cpu(), s.cpu()
+    parts = torch.nn.functional.pad(y, (0, n * g - c)).reshape(r, n, g)
+    scale = parts.abs().amax(2) * torch.tensor(1 / O.FMAX[ykind])
+    assert torch.equal(s, scale)
+    ref = (parts / scale[:, :, None]).reshape(r, n * g)[:, :c].clamp(-O.FMAX[ykind], O.FMAX[ykind]).to(T[ykind])
+    off = q.view(torch.uint8) != ref.view(torch.uint8)
+    assert int(off.sum()) == 0, f"{int(off.sum())} of {off.numel()}"
+
+
+@pytest.mark.parametrize("ykind", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("c", [64, 5000, 20000])
+@pytest.mark.parametrize("group", [0, 32])
+def test_norm_8bit_infinity(ykind, c, group):
+    """An infinite y makes its group's scale infinite, itself a NaN and the rest of the group zeros."""
+    x, w = torch.ones(3, c, device="cuda"), torch.ones(c, device="cuda")
+    w[37] = float("inf")
+    g = group or c
+    q, s = torch.empty(3, c, device="cuda", dtype=T[ykind]), torch.empty(3, -(-c // g), device="cuda")
+    K.muon_norm_forward(x, q, weight=w, scales=s, group=group, eps=EPS)
+    q, k = q.float().cpu(), 37 // g
+    assert bool(s[:, k].isinf().all()) and int(s.isinf().sum()) == 3
+    inside = torch.arange(c) // g == k
+    assert bool(q[:, 37].isnan().all()) and int(q.isnan().sum()) == 3
+    assert bool((q[:, inside & (torch.arange(c) != 37)] == 0).all())
+    assert bool((q[:, ~inside] == O.FMAX[ykind]).all())
