@@ -653,8 +653,8 @@ __global__ __launch_bounds__(RT) void route_bwd(muon_route_spec s, muon_route_gr
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         if (!(l[i] > -HUGE_VALF)) continue;
-        const float q = one_less_sigmoid(l[i]);
-        d[i] += ds[i] * (1.f - q) * q;
+        const float e = expf(-fabsf(l[i]));   // s (1 - s) without a difference
+        d[i] += ds[i] * (e / ((1.f + e) * (1.f + e)));
       }
     }
   }

@@ -224,6 +224,31 @@ def test_route_backward_masks(score, renorm):
         check_backward(l, route, idx, w, ds, rng, pad=9, shift=3)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("e,k", [(8, 2), (64, 6), (256, 8), (1000, 10)])
+def test_route_backward_sigmoid_small_scores(e, k, renorm, kind):
+    """dscores s (1 - s) of experts whose scores are small keeps its leading digits: logits from -60 to 10, and
+    no term of the other experts in the bound."""
+    rng = np.random.default_rng(e)
+    l = torch.from_numpy(rng.uniform(-60, 10, (40, e)).astype(np.float32)).cuda().to(T[kind])
+    l[0], l[1] = -40.0, -8.0
+    route = K.Route(k, "sigmoid", renormalise=renorm, scale=2.5)
+    idx, w, _ = run(l, route)
+    dw = torch.from_numpy(rng.standard_normal((40, k)).astype(np.float32)).cuda()
+    ds = torch.from_numpy(rng.standard_normal((40, e)).astype(np.float32)).cuda()
+    dl = torch.empty_like(l)
+    K.muon_route_backward(route, l, idx, w, dw, dl, dscores=ds)
+    i, wv = idx.cpu().numpy().astype(np.int64), f64(w)
+    ref = O.route_backward(f64(l), i, wv, f64(dw), "sigmoid", renorm, 2.5, f64(ds))
+    lead = wv * np.abs(f64(dw))
+    lead = lead + (wv / 2.5 * lead.sum(1, keepdims=True) if renorm else 0)
+    s = 1 / (1 + np.exp(-f64(l)))
+    terms = s * (1 - s) * np.abs(f64(ds))
+    np.add.at(terms, (np.arange(40)[:, None], i), lead)
+    assert np.all(np.abs(f64(dl) - ref) <= HALF[kind] * np.abs(ref) * (1 + 2.0 ** -8) + REL * terms)
+
+
 @pytest.mark.parametrize("t", [1, 5, 64, 3000])
 def test_route_backward_rows(t):
     rng = np.random.default_rng(t)
