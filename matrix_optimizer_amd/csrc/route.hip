@@ -324,6 +324,11 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
     float* of_l = by_l + E;
     int* in_l = reinterpret_cast<int*>(of_l + G);
     const int n = E / G, span = n / 8;
+    float size = 0.f;   // the row's largest |b1| + |b2|, the terms of a value
+    auto value = [&](float b1, float b2) {
+      if (b1 > -HUGE_VALF) size = fmaxf(size, fabsf(b1) + (b2 > -HUGE_VALF ? fabsf(b2) : 0.f));
+      return s.group_top == 2 && b2 > -HUGE_VALF ? b1 + b2 : b1;
+    };
     // groups of 8 span experts, span a power of two up to a row's lanes: the
     // same chunk of `span` neighbouring lanes, whose two best meet by exchange
     const bool lanes = n % 8 == 0 && (span & (span - 1)) == 0 && span <= LPT;
@@ -347,7 +352,8 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
         if (span > 16) meet(__shfl_xor(b1, 16, WAVE), __shfl_xor(b2, 16, WAVE));
         if (span > 32) meet(__shfl_xor(b1, 32, WAVE), __shfl_xor(b2, 32, WAVE));
         const int g = (i * LPT + t) / span;
-        if ((t & (span - 1)) == 0 && g < G) of_l[g] = s.group_top == 2 && b2 > -HUGE_VALF ? b1 + b2 : b1;
+        const float of = value(b1, b2);
+        if ((t & (span - 1)) == 0 && g < G) of_l[g] = of;
       }
     } else {   // a lane a group, over its experts in shared memory
 #pragma unroll
@@ -363,14 +369,19 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
           b2 = fmaxf(b2, fminf(b1, x));
           b1 = fmaxf(b1, x);
         }
-        of_l[g] = s.group_top == 2 && b2 > -HUGE_VALF ? b1 + b2 : b1;
+        of_l[g] = value(b1, b2);
       }
     }
     wave_sync();
+    // How near two values may be: their scores' part is 2 tol; a value is off by
+    // 2^-24 of `size` for its sum, by as much again where a bias is added to its
+    // terms, the other value likewise, and the comparison rounds once.  (Large
+    // biases of opposite signs leave a small value with a large error.)
+    const float far = 2.f * tol + (a.bias ? 0x1p-21f : 0x1p-22f) * over_row<LPT>(size, max_f);
     // a group is in if fewer than top_groups may be before it, out if as many
     // surely are; one without an open expert is of no matter
     for (int g = t; g < G; g += LPT) {
-      const float mine = of_l[g], far = 2.f * tol + 0x1p-21f * fabsf(mine);
+      const float mine = of_l[g];
       int sure = 0, may = 0;
       if (mine > -HUGE_VALF) {
         for (int q = 0; q < G; ++q) {

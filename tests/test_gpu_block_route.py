@@ -163,6 +163,46 @@ def test_route_wide_values(score, e):
         check(logits_of(rng, 25, e, "bf16"), K.Route(7, score, 2, 1), bias)
 
 
+def choose(l, bias, route):
+    """The experts of route's rule for many rows without closed experts, in 64 bits."""
+    t, e = l.shape
+    if route.score == "sigmoid":
+        s = 1 / (1 + np.exp(-l))
+    else:
+        s = np.exp(l - l.max(1, keepdims=True))
+        s = s / s.sum(1, keepdims=True)
+    rank = s + bias
+    n = e // route.groups
+    best = -np.sort(-rank.reshape(t, route.groups, n), axis=2)[:, :, :route.group_top]
+    out = np.argsort(-best.sum(2), axis=1, kind="stable")[:, route.top_groups:]
+    hidden = np.zeros((t, route.groups), bool)
+    np.put_along_axis(hidden, out, True, 1)
+    rank = np.where(np.repeat(hidden, n, axis=1), -np.inf, rank)
+    return np.argsort(-rank, axis=1, kind="stable")[:, :route.top_k]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("far", [10.0, 1e3, 1e5, 1e6])
+@pytest.mark.parametrize("n,g,tg", [(2, 2, 1), (5, 6, 2), (8, 4, 1), (16, 8, 3), (64, 4, 2), (128, 8, 3)])
+def test_route_groups_whose_biases_cancel(n, g, tg, far, score):
+    """A group's value is a small sum of large terms where its two best have biases of opposite sign: the rounding
+    of the terms, not of the sum, decides how near two groups may be."""
+    rng = np.random.default_rng(n * g)
+    t = 20000 if n * g <= 32 else 2000
+    bias = np.full((g, n), -2 * far, np.float32)
+    bias[0::2, :2] = far, -far
+    bias[1::2, :2] = 0
+    bias = bias.reshape(-1)
+    # scores of a group's two best so near those of the next that fp32 sums of this size do not tell them apart
+    l = rng.standard_normal((t, g * n)).astype(np.float32) * np.float32(0.5)
+    if score == "softmax":
+        l.reshape(t, g, n)[:, :, :2] += 4
+    route = K.Route(2, score, g, tg, 2)
+    idx = run(torch.from_numpy(l).cuda(), route, torch.from_numpy(bias).cuda(), scores=False)[0]
+    wrong = (idx.cpu().numpy() != choose(l.astype(np.float64), bias.astype(np.float64), route)).any(1)
+    assert not wrong.any(), f"{int(wrong.sum())} of {t} rows"
+
+
 # ---- backward ---------------------------------------------------------------
 def check_backward(logits, route, idx, w, dscores=False, rng=None, pad=0, shift=0):
     t, e = logits.shape
