@@ -146,8 +146,9 @@ muon_status muon_norm_workspace_bytes(int64_t rows, int64_t cols, size_t* out);
  *   weight scale s, or with renormalise scale s / (sum of the chosen s),
  *          which is formed from differences of log s and so holds where every
  *          s underflows.
- * The bias is finite.  Limits: E <= 1024, top_k <= 32, top_k <= top_groups
- * E / groups. */
+ * The bias is finite; with a NaN or an infinity in it the chosen experts are
+ * still distinct and in range, but not further specified.  Limits: E <= 1024,
+ * top_k <= 32, top_k <= top_groups E / groups. */
 typedef enum { MUON_SCORE_SOFTMAX = 0, MUON_SCORE_SIGMOID = 1 } muon_score;
 #define MUON_ROUTE_MAX_EXPERTS 1024
 #define MUON_ROUTE_MAX_TOP_K 32

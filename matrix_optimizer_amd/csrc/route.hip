@@ -528,6 +528,8 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
         x = exp(soft ? x - (double)top : -x);
         x = soft ? x / total : 1.0 / (1.0 + x);
         x += (double)a.bias[chosen[c]];
+        // a NaN, which a bias may bring, is last: each expert needs a place of its own
+        x = x == x ? x : kOut;
       }
       val[c] = x;
     }

@@ -203,6 +203,26 @@ def test_route_groups_whose_biases_cancel(n, g, tg, far, score):
     assert not wrong.any(), f"{int(wrong.sum())} of {t} rows"
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e,k,g", [(8, 4, 1), (30, 6, 1), (64, 6, 8), (256, 8, 8), (256, 8, 1), (1024, 32, 4)])
+def test_route_bias_not_finite(e, k, g, score):
+    """A bias that is NaN or infinite chooses no expert twice and none that there is not, also where equal values
+    are put in order in 64 bits; rows of other calls are not concerned."""
+    for far in (float("nan"), float("inf"), -float("inf")):
+        for every in (1, 2, 3):
+            bias = torch.zeros(e, device="cuda")
+            bias[::every] = far
+            for l in (torch.zeros(33, e, device="cuda"), torch.randn(33, e, device="cuda").bfloat16()):
+                idx, w, _ = run(l, K.Route(k, score, g, max(1, g // 2)), bias, scores=False)
+                got = idx.cpu().numpy()
+                assert got.min() >= -1 and got.max() < e
+                for row in got:
+                    on = row[row >= 0]
+                    assert len(set(on)) == len(on)
+                w = w.cpu().numpy()
+                assert np.isfinite(w).all() and (w >= 0).all() and (w[got < 0] == 0).all()
+
+
 # ---- backward ---------------------------------------------------------------
 def check_backward(logits, route, idx, w, dscores=False, rng=None, pad=0, shift=0):
     t, e = logits.shape
