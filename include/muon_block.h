@@ -144,8 +144,8 @@ muon_status muon_norm_workspace_bytes(int64_t rows, int64_t cols, size_t* out);
  *          where fewer than top_k experts are open, and in rows whose
  *          token_mask byte is 0;
  *   weight scale s, or with renormalise scale s / (sum of the chosen s),
- *          which is formed from differences of log s and so holds where every
- *          s underflows.
+ *          which holds where some s or all of them underflow: it is formed
+ *          from differences of log s there.
  * The bias is finite; with a NaN or an infinity in it the chosen experts are
  * still distinct and in range, but not further specified.  Limits: E <= 1024,
  * top_k <= 32, top_k <= top_groups E / groups. */

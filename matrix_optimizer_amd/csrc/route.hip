@@ -552,19 +552,21 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
   constexpr int SLOTS = (MUON_ROUTE_MAX_TOP_K + LPT - 1) / LPT;
   int at[SLOTS];
   float p[SLOTS], sum = 0.f;
-  bool any = false;
+  bool tiny = false;
 #pragma unroll
   for (int j = 0; j < SLOTS; ++j) {
     const int k = t + j * LPT;
     at[j] = k < K ? chosen[k] : -1;
     p[j] = 0.f;
     if (at[j] < 0) continue;
-    any = true;
     p[j] = slot_score(read_logit(ld_as_f32(row, at[j])), top, soft);
+    tiny |= p[j] < 0x1p-120f;
     sum += p[j];
   }
   sum = over_row<LPT>(sum, add_f);
-  if (s.renormalise && any && !(sum > 0x1p-100f)) unsure = true;   // every score underflows: by logarithms
+  // a score near or below the normal range whose share of a small sum is not
+  // small: by logarithms
+  if (s.renormalise && tiny && sum < 0.5f) unsure = true;
   const float by = s.renormalise ? sum : z;
 #pragma unroll
   for (int j = 0; j < SLOTS; ++j) {

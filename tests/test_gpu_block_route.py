@@ -223,6 +223,27 @@ def test_route_bias_not_finite(e, k, g, score):
                 assert np.isfinite(w).all() and (w >= 0).all() and (w[got < 0] == 0).all()
 
 
+@pytest.mark.parametrize("low", [(-60, -69, -92, -104), (-69, -100, -100, -75), (-60, -104, -110, -140),
+                                 (-80, -81, -95, -170), (-40, -90, -100, -130), (-3, -90, -101, -120)])
+def test_route_weights_of_widely_spread_small_scores(low):
+    """Renormalised weights hold where the smaller chosen scores are below fp32's normal range and their ratios to
+    the others are not."""
+    l = torch.tensor([low], dtype=torch.float32, device="cuda").repeat(5, 1)
+    l += torch.arange(5, device="cuda")[:, None] * 0.37
+    check(l, K.Route(4, "sigmoid", scale=2.5))
+    check(l.bfloat16(), K.Route(4, "sigmoid"))
+    # chosen far below the largest score: by a bias, and by the groups
+    for e in (16, 64, 256):
+        wide = torch.zeros(5, e, device="cuda")
+        wide[:, 1:] = -200.0
+        wide[:, 4:8] = l
+        bias = torch.zeros(e, device="cuda")
+        bias[4:8] = 3.0
+        for score in ("softmax", "sigmoid"):
+            check(wide, K.Route(4, score, scale=0.5), bias)
+            check(wide, K.Route(4, score, e // 4, 1, 1), bias)
+
+
 # ---- backward ---------------------------------------------------------------
 def check_backward(logits, route, idx, w, dscores=False, rng=None, pad=0, shift=0):
     t, e = logits.shape
