@@ -42,7 +42,7 @@ class MoEBlock:
         self.gain = torch.ones(hidden, device="cuda")
         self.dgain = torch.empty_like(self.gain)
         self.bias = torch.zeros(experts, device="cuda")
-        self.rooms = {}
+        self.rooms, self.last = {}, None
 
     def _view(self, i, buffers):
         """Parameter i inside the batch buffers (its matrices are one run of one batch here)."""
@@ -69,7 +69,7 @@ class MoEBlock:
     def forward_backward(self, x, residual, target, step=0):
         """(loss, dx, dresidual); the parameters' gradients are left in dR, dW1, dW2, dgain."""
         T, k = x.shape[0], self.k
-        m = self._room(T)
+        m = self.last = self._room(T)
         drop = K.Dropout(self.p, self.seed, step)
         K.muon_norm_forward(x, m["y"], residual=residual, h=m["h"], weight=self.gain, rstd=m["rstd"], dropout=drop)
         logits = m["y"] @ self.R.t()
@@ -110,8 +110,7 @@ class MoEBlock:
     def update(self, rate=1e-3, gain_lr=0.1):
         self.muon.step()
         self.gain.add_(self.dgain, alpha=-gain_lr)
-        counts = next(iter(self.rooms.values()))["counts"]
-        K.muon_route_balance(counts, self.bias, self.bias, rate)
+        K.muon_route_balance(self.last["counts"], self.bias, self.bias, rate)   # of the last forward_backward
 
 
 def main(argv=None):

@@ -52,6 +52,19 @@ def test_gradients_match_autograd():
         assert off < 0.03, (name, float(off))
 
 
+def test_update_uses_the_last_call():
+    """Steps of several row counts in turn: the bias follows the counts of the step before each update."""
+    b = X.MoEBlock(hidden=64, inner=96, experts=8, top_k=2, groups=2, top_groups=1, seed=3)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    for step, rows in enumerate((50, 37, 120, 50)):
+        x, r = (torch.randn(rows, 64, generator=g, device="cuda").bfloat16() for _ in range(2))
+        b.forward_backward(x, r, torch.randn(rows, 64, generator=g, device="cuda"), step)
+        counts, before = b.rooms[rows]["counts"].cpu().numpy(), b.bias.double().cpu().numpy()
+        assert counts.sum() == rows * 2
+        b.update(rate=0.125)
+        assert np.array_equal(b.bias.double().cpu().numpy(), O.route_balance(counts, before, 0.125)), step
+
+
 def test_steps_lower_the_loss():
     losses = X.main(["--steps", "12", "--rows", "512"])
     assert all(np.isfinite(losses)) and losses[-1] < 0.8 * losses[0]
