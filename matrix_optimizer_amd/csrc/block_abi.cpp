@@ -143,6 +143,7 @@ muon_status muon_dropout(int64_t rows, int64_t cols, const void* x, int64_t x_st
   Buffers b;
   const int ix = b.matrix(x, rows, cols, x_stride, size_of(dtype), false);
   const int iy = b.matrix(y, rows, cols, y_stride, size_of(dtype), true);
+  if (d.dev) b.flat(d.dev, 2, 8, false);
   if ((st = b.check({{ix, iy}})) != MUON_OK) return st;
   return hip_status(run_dropout(rows, cols, x, x_stride, y, y_stride, dtype, d, hip_stream(stream)));
 }

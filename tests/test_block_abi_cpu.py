@@ -130,6 +130,20 @@ def test_dropout_refusals(mem):
     assert call(rows=0) == B.MUON_OK
 
 
+def test_dropout_seed_apart_from_the_output(mem):
+    """{seed, offset} on the device may be neither inside y nor inside an x that is y, as in the norm's calls."""
+    L = K.lib()
+
+    def call(seed, y=mem(1)):
+        spec = K.muon_dropout_spec(0.5, 1, 1, seed)
+        return L.muon_dropout(4, 64, mem(0), 64, y, 64, 0, C.byref(spec), None)
+
+    assert call(mem(1)) == call(mem(1) + 1016) == call(mem(1) - 8) == call(mem(0) + 8, mem(0)) == INVALID
+    assert call(mem(1) + 4) == INVALID                                  # not 8-byte aligned
+    # apart, or inside an input: these reach the launch, which fails here
+    assert call(mem(1) + 1024) == call(mem(1) - 16) == call(mem(0)) == B.MUON_ERR_HIP
+
+
 def _route(mem, spec=None, **over):
     s = K.muon_route_spec(1, 4, 4, 2, 2, 1, 1.0)
     for k, v in (spec or {}).items():
