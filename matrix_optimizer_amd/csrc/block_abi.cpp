@@ -259,7 +259,7 @@ muon_status muon_route_backward(const muon_route_spec* s, const muon_route_grad_
 
 muon_status muon_route_order_workspace_bytes(int64_t num_pairs, int64_t num_experts, size_t* out) {
   if (!out || num_pairs < 0 || num_experts < 1) return MUON_ERR_INVALID_ARG;
-  if (num_pairs > kMaxPairs || num_experts > MUON_ROUTE_MAX_EXPERTS) return MUON_ERR_UNSUPPORTED;
+  if (num_pairs >= kMaxPairs || num_experts > MUON_ROUTE_MAX_EXPERTS) return MUON_ERR_UNSUPPORTED;
   *out = order_bytes(num_pairs, num_experts);
   return MUON_OK;
 }

@@ -217,6 +217,13 @@ def test_order_and_balance_refusals(mem):
     assert bal(n=1025) == UNSUPPORTED
 
 
+def test_order_largest_number_of_pairs():
+    """num_pairs < 2^31 - 2^16."""
+    L, out, most = K.lib(), C.c_size_t(7), (1 << 31) - (1 << 16)
+    assert L.muon_route_order_workspace_bytes(most, 256, C.byref(out)) == UNSUPPORTED and out.value == 7
+    assert L.muon_route_order_workspace_bytes(most - 1, 256, C.byref(out)) == B.MUON_OK and out.value > 7
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     x = torch.zeros(2, 8)
     with pytest.raises(ValueError):
