@@ -17,10 +17,10 @@ constexpr int NT = 256;            // threads of a workgroup
 constexpr int64_t kMaxGrid = 1 << 16;
 
 // D(x) alone: eight columns a lane, which share one Philox block, 16 bits an
-// element.  [8192, 28672] bf16: 163 us, 5.8 TB/s, the vector units busy 74 % of
-// it with one block; 32 bits an element would need two.  WHOLE: a width of
-// whole chunks, which spares the tests for the last one ([16384, 4096] bf16
-// 49 us, 52 with them).
+// element.  [8192, 28672] bf16: 162 us a call among others, 5.8 TB/s, the vector
+// units busy 75 % of it with one block; 32 bits an element would need two.
+// WHOLE: a width of whole chunks, which spares the tests for the last one
+// ([16384, 4096] bf16 48 us, 52 with them; 4095 columns 57).
 template <typename T, bool WHOLE>
 __global__ __launch_bounds__(NT) void dropout_k(int64_t rows, int64_t cols, const T* x, int64_t xs, T* y, int64_t ys,
                                                 Drop d) {
@@ -140,8 +140,8 @@ struct RowLanes {
 // issued before this row's reduction and stores, so that memory is busy
 // meanwhile.  Measured: [16384, 4096] bf16 with residual and p = 0.1 98 us,
 // 5.5 TB/s (two passes over the row 135); [4096, 8192] to e4m3 with a scale per
-// 128 columns 45.6 us, 5.2 TB/s; [65536, 128] 13 us; one row of 4096 3.2 us, less
-// than the call.
+// 128 columns 45.6 us, 5.2 TB/s; [65536, 128] 12.5 us; fp32 [8192, 4096] 97 us,
+// [4096, 16384] bf16 103 us; one row of 4096 3.2 us, less than the call.
 template <typename T, int NC, int LPR>
 __global__ __launch_bounds__(LPR ? NT : 512) void norm_fwd(muon_norm_args a, Drop d) {
   __shared__ GroupRed sums, maxima;
@@ -225,7 +225,8 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_fwd(muon_norm_args a, Dro
 }
 
 // Rows longer than the registers hold: z is formed again in each pass over
-// the row, which the caches mostly hold by then.
+// the row, which the caches mostly hold by then.  [2048, 28672] bf16 with
+// residual 133 us, 3.5 TB/s: the second pass is not free.
 template <typename T>
 __global__ __launch_bounds__(512) void norm_fwd_long(muon_norm_args a, Drop d) {
   __shared__ GroupRed sums, maxima;
@@ -278,10 +279,11 @@ __global__ __launch_bounds__(512) void norm_fwd_long(muon_norm_args a, Drop d) {
 // Backward, the row in registers as in norm_fwd.  dweight's sums stay in the
 // lanes' registers over all of a workgroup's rows; each workgroup leaves one
 // row of partial sums (or the result, if it is the only one).  [16384, 4096]
-// bf16 with dropout and dh: 126 us and 5 for norm_dw_sum, 5.1 TB/s of the
+// bf16 with dropout and dh: 128 us and 5 for norm_dw_sum, 5.0 TB/s of the
 // bytes without the partial sums (passes of their own for dz and dweight 346);
-// [777, 2051] fp32 in a wider buffer 10 + 4 us, the latency of four rows in a
-// row and of two launches.
+// fp32 [8192, 4096] 73 + 5, bf16 [4096, 8200] 51 + 5 and [4096, 16384] 81 + 5
+// (four chunks a lane and no loads ahead: 4.7 TB/s); [777, 2051] fp32 in a
+// wider buffer 11 + 4 us, the latency of four rows in a row and of two launches.
 template <typename T, int NC, int LPR>
 __global__ __launch_bounds__(LPR ? NT : 512) void norm_bwd(muon_norm_grad_args a, Drop d, float* parts) {
   __shared__ GroupRed sums;
@@ -389,7 +391,8 @@ __global__ __launch_bounds__(LPR ? NT : 512) void norm_bwd(muon_norm_grad_args a
 }
 
 // Rows longer than the registers hold: two passes over the row, and dweight's
-// partial sums (a row of `parts` for each workgroup, its own lanes' columns) in memory.
+// partial sums (a row of `parts` for each workgroup, its own lanes' columns) in
+// memory.  [2048, 28672] bf16 171 + 6 us, 2.0 TB/s of the bytes.
 template <typename T>
 __global__ __launch_bounds__(512) void norm_bwd_long(muon_norm_grad_args a, Drop d, float* parts) {
   __shared__ GroupRed sums;
@@ -515,18 +518,19 @@ int64_t even(int64_t groups, int64_t most) {
 // CUs where a lane keeps one chunk, two workgroups where it keeps more.
 // [16384, 4096] bf16 with p = 0.1: half as many 6 % slower, twice as many 3 %
 // (the last round of workgroups is then part empty); [3777, 2880] by three
-// workgroups of 384 lanes 20 us, by two or four 24 (a fourth does not fit the
-// SIMD that holds two waves of each).
+// workgroups of 384 lanes 20 us a call, by two or four 24 (a fourth does not fit
+// the SIMD that holds two waves of each; 17 us of it are the kernel's).
 int64_t resident(const RowShape& s) { return 256 * (s.nc == 1 ? (1024 + s.threads - 1) / s.threads : 1024 / s.threads); }
 
 }  // namespace
 
 // Backward: each workgroup leaves a row of partial sums, written and read
 // again, which costs as much as parts / rows of the whole.  As many as keep
-// the memory busy, 1024 lanes a CU ([12010, 1728] bf16: 39 us, 53 by half), as
-// long as each has 12 rows; one a CU where a lane keeps more chunks ([4096,
-// 8192]: 43 us, two 48); up to 4 rows in a row a single one, which needs no
-// second launch.
+// the memory busy, 1024 lanes a CU ([12010, 1728] bf16 with dh: 39 us, 53 by
+// half), as long as each has 12 rows; one a CU where a lane keeps more chunks
+// ([4096, 8192]: 44 us, two 48; it leaves a CU five waves just past 4096 columns,
+// [16384, 4097] 115 us where 4096 take 78); up to 4 rows in a row a single one,
+// which needs no second launch.
 int64_t norm_parts(int64_t rows, int64_t cols) {
   const RowShape s = row_shape(cols);
   const int64_t groups = (rows + s.per_group - 1) / s.per_group;

@@ -213,8 +213,8 @@ __host__ __device__ constexpr int route_wave_words(int E, int G, int rows, int c
 //
 // The choice is defined on scores in 64 bits; forming and sorting them so took
 // 275 us for 32768 rows of 256 experts in 8 groups, of which the bytes are 4;
-// now 21 us (15 without groups, 10 without bias), 14 of them vector
-// instructions, 1030 a wave.
+// now 20 to 22 us by sigmoid with a bias (16 without groups; by softmax 27 and
+// 20; 11 without bias and groups), 14.7 of them vector instructions, 1060 a wave.
 // What bounds it is the instructions of the choice, and at the end the longest
 // wave, so a row gets 4 to 64 lanes (16 for 256 experts, four rows a wave),
 // and the choice is made in three grades, each for the rows that the one
@@ -223,7 +223,7 @@ __host__ __device__ constexpr int route_wave_words(int E, int G, int rows, int c
 //      numbers differ and the next largest is the least of m - 1 - number as
 //      unsigned: 1.5 instructions an expert, nothing is marked.  bf16 logits
 //      fit whole; other values must differ in those bits (scores by their
-//      error), which all but about one row in 350 do;
+//      error), which most rows' do;
 //   2. the experts taken, and those after them that their bits do not set
 //      apart, in 64 bits, a lane each, and put in order by counting;
 //   3. route_row_64.
@@ -426,7 +426,7 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
     int num[V];
     int m = kNone;
     // 22 bits of a value: a bf16 logit's ordered key, or steps below the
-    // largest, of 2^-20 in a range of 2 for scores and of 2^-17 in 32 for
+    // largest, of 2^-20 in a range of 2 for scores and of 2^-17 in 16 for
     // logits; values are in order where their steps differ, and scores where
     // these differ by `apart`
     const int low = (~t & (LPT - 1)) * 8;   // 1023 - e in bits: those of t, chunk and element reversed
@@ -587,7 +587,7 @@ __global__ __launch_bounds__(RT, 5) void route_fwd(muon_route_spec s, muon_route
 
 // A wave's rows' gradients.  The chosen experts' a_k reach their columns by
 // way of shared memory; the logits are read only where a dense term needs them.
-// 32768 rows of 64 experts with dscores 6.5 us, 256 experts 15 us, 4.4 TB/s
+// 32768 rows of 64 experts with dscores 7.1 us, 256 experts 16 us, 4.4 TB/s
 // (rows as wide as a wave with scalar loads: 31 us for 64).
 template <typename T, int LPT, int NC>
 __global__ __launch_bounds__(RT) void route_bwd(muon_route_spec s, muon_route_grad_args a) {
@@ -693,7 +693,7 @@ __global__ __launch_bounds__(RT) void route_bwd(muon_route_spec s, muon_route_gr
 // time: lanes of one expert find each other by a ballot for each bit of the
 // expert's number, and the lane's rank among them and the pairs of the wave
 // before is its place among the wave's.  One tile needs order_place alone.
-// 1M pairs of 256 experts: 3.6 + 14 us, of which the bytes are 2.5; what is
+// 1M pairs of 256 experts: 4 to 5 + 14.5 us, of which the bytes are 2.5; what is
 // left is latency, one workgroup a CU going through six steps with barriers
 // between (counts one at a time 57 us, stores straight to `order` 2.5 us more).
 constexpr int OT = 1024, OW = OT / WAVE;

@@ -24,7 +24,7 @@ __device__ __forceinline__ void unpack8(const u32x4& v, float* f) {
 // (c may lie past it): 4 registers of bf16 or 8 of fp32, so that loads can be
 // in flight while the row before is worked on.  The row's last chunk is the
 // row's last eight columns, moved down by get() and not before, since that
-// waits for them ([16384, 4095] bf16: norm forward and backward 123 and 96 us,
+// waits for them ([16384, 4095] bf16: norm forward and backward 123 and 95 us,
 // 191 and 161 with a load for each column behind its own test).
 typedef uint16_t u16_any __attribute__((aligned(1)));
 typedef uint32_t u32_any __attribute__((aligned(1)));
