@@ -16,7 +16,8 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libmuon.so")
 
 SOURCES = ["abi.cpp", "trace.cpp", "schedule.cpp", "skinny.hip", "tiled.hip", "noalloc.hip", "block_abi.cpp",
-           "norm.hip", "route.hip"]
+           "norm.hip", "route.hip", "experts_abi.cpp", "places.hip", "gate.hip", "quantise.hip", "product.hip",
+           "weight_grad.hip"]
 ARCH = "gfx950"
 FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

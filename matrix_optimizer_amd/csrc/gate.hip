@@ -1,0 +1,109 @@
+// The gated activation between an expert's two products and its gradient
+// (gfx950), one pass over the rows each: bound by the bytes they move.
+#include <cmath>
+
+#include "experts_rows.h"
+
+namespace muon {
+namespace {
+
+// s = sigmoid(g) and 1 - s, both without cancellation: with t = e^-|g|, s is
+// 1 / (1 + t) or t / (1 + t).
+__device__ __forceinline__ void sigmoids(float g, float& s, float& rest) {
+  const float t = expf(-fabsf(g)), r = 1.f / (1.f + t), q = t * r;
+  s = g >= 0.f ? r : q;
+  rest = g >= 0.f ? q : r;
+  if (g != g) s = rest = g;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+ex_gate_forward(muon_gate_args a, int log_lanes) {
+  const int lanes = 1 << log_lanes, lane = threadIdx.x & (lanes - 1), per = 256 >> log_lanes;
+  const int64_t rows = rows_in_use(a.rows, a.used), step = (int64_t)gridDim.y * lanes * 8;
+  const bool e5 = a.y8_dtype == MUON_ROW_E5M2;
+  for (int64_t r = (int64_t)blockIdx.x * per + (threadIdx.x >> log_lanes); r < rows; r += (int64_t)gridDim.x * per) {
+    const T* gr = static_cast<const T*>(a.a) + r * a.a_stride;
+    for (int64_t b = (int64_t)blockIdx.y * lanes * 8; b < a.cols; b += step) {
+      const int64_t c = b + lane * 8;   // may pass the row's end: a group's lanes stay together
+      float g[8], u[8];
+      load8(gr, c, a.cols, g);
+      load8(gr + a.cols, c, a.cols, u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float s, rest;
+        sigmoids(g[e], s, rest);
+        u[e] *= g[e] * s;
+      }
+      if (a.y && c < a.cols) store8(static_cast<T*>(a.y) + r * a.y_stride, c, a.cols, u);
+      if (a.y8) {
+        const float scale = group_scale(over_row<16>(most8(u), max_f), e5);
+        if (c < a.cols) {
+          if ((c & 127) == 0) a.scales[r * a.scales_stride + (c >> 7)] = scale;
+          store_eight(static_cast<uint8_t*>(a.y8) + r * a.y8_stride, c, a.cols, u, scale, e5);
+        }
+      }
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+ex_gate_backward(muon_gate_grad_args a, int log_lanes) {
+  const int lanes = 1 << log_lanes, lane = threadIdx.x & (lanes - 1), per = 256 >> log_lanes;
+  const int64_t rows = rows_in_use(a.rows, a.used), step = (int64_t)gridDim.y * lanes * 8;
+  const bool e5 = a.da8_dtype == MUON_ROW_E5M2;
+  for (int64_t r = (int64_t)blockIdx.x * per + (threadIdx.x >> log_lanes); r < rows; r += (int64_t)gridDim.x * per) {
+    const T* gr = static_cast<const T*>(a.a) + r * a.a_stride;
+    for (int64_t b = (int64_t)blockIdx.y * lanes * 8; b < a.cols; b += step) {
+      const int64_t c = b + lane * 8;
+      float g[8], u[8], d[8];
+      load8(gr, c, a.cols, g);
+      load8(gr + a.cols, c, a.cols, u);
+      load8(static_cast<const T*>(a.dy) + r * a.dy_stride, c, a.cols, d);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float s, rest;
+        sigmoids(g[e], s, rest);
+        const float du = d[e] * (g[e] * s);
+        g[e] = d[e] * u[e] * (s * __builtin_fmaf(g[e], rest, 1.f));
+        u[e] = du;
+      }
+      if (a.da && c < a.cols) {
+        T* row = static_cast<T*>(a.da) + r * a.da_stride;
+        store8(row, c, a.cols, g);
+        store8(row + a.cols, c, a.cols, u);
+      }
+      if (a.da8) {   // cols is a multiple of 128
+        const float sg = group_scale(over_row<16>(most8(g), max_f), e5), su = group_scale(over_row<16>(most8(u), max_f), e5);
+        if (c < a.cols) {
+          if ((c & 127) == 0) {
+            a.scales[r * a.scales_stride + (c >> 7)] = sg;
+            a.scales[r * a.scales_stride + ((a.cols + c) >> 7)] = su;
+          }
+          uint8_t* row = static_cast<uint8_t*>(a.da8) + r * a.da8_stride;
+          store_eight(row, c, a.cols, g, sg, e5);
+          store_eight(row + a.cols, c, a.cols, u, su, e5);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t run_gate_forward(const muon_gate_args& a, hipStream_t stream) {
+  const RowLayout l = row_layout(a.rows, (a.cols + 7) / 8);
+  if (a.dtype == MUON_F32) ex_gate_forward<float><<<dim3(l.gx, l.gy), 256, 0, stream>>>(a, l.log_lanes);
+  else ex_gate_forward<bf16_t><<<dim3(l.gx, l.gy), 256, 0, stream>>>(a, l.log_lanes);
+  return hipGetLastError();
+}
+
+hipError_t run_gate_backward(const muon_gate_grad_args& a, hipStream_t stream) {
+  const RowLayout l = row_layout(a.rows, (a.cols + 7) / 8);
+  if (a.dtype == MUON_F32) ex_gate_backward<float><<<dim3(l.gx, l.gy), 256, 0, stream>>>(a, l.log_lanes);
+  else ex_gate_backward<bf16_t><<<dim3(l.gx, l.gy), 256, 0, stream>>>(a, l.log_lanes);
+  return hipGetLastError();
+}
+
+}  // namespace muon

@@ -94,17 +94,7 @@ __device__ __forceinline__ void store_y(const muon_norm_args& a, int64_t r, I c,
       scale = scale_of(most, a.y_dtype);
       if (c < cols && (c & (a.group - 1)) == 0) a.scales[r * a.scales_stride + c / a.group] = scale;
     }
-    // y / scale as fp32 divides (but for one in a million, an ulp off): 1 / scale
-    // in two floats, the first a little too small so that the second is positive
-    // and -0 keeps its sign.  2^-126 <= scale < 2^120, or infinite: then finite
-    // elements become 0 and infinite ones NaN.  One multiplication more an
-    // element than by the reciprocal alone, which moves a few in a million by an
-    // 8-bit step: [4096, 8192] 45.6 us against 45.4, [32768, 1024] by groups of 32
-    // 24.2 against 23.6.
-    const float inv = __builtin_amdgcn_rcpf(scale) * (1.f - 0x1p-22f);
-    const float rest = scale < HUGE_VALF ? __builtin_fmaf(-scale, inv, 1.f) * inv : 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(y[j], inv, y[j] * rest);
+    quotients8(y, scale);
     uint8_t* row = static_cast<uint8_t*>(a.y) + r * a.y_stride;
     if (c < cols) {
       if (e5) store8_8bit<true>(row, c, cols, y);

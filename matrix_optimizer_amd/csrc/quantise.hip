@@ -1,0 +1,83 @@
+// Matrices in 8 bits by blocks of 128 x 128, as they are and transposed
+// (gfx950): one pass, a workgroup a block.
+#include "experts_rows.h"
+
+namespace muon {
+namespace {
+
+// A block stays in registers between its maximum and its values (64 a lane:
+// eight rows of eight columns), so x is read once; the transposed copy goes
+// through shared memory.
+template <typename T>
+__global__ void __launch_bounds__(256)
+ex_quantise(muon_quantise_args a, int64_t rb, int64_t cb) {
+  __shared__ GroupRed red;
+  __shared__ uint8_t tile[128][132];
+  const int t = threadIdx.x, cc = (t & 15) * 8, rr = t >> 4;
+  const bool e5 = a.q_dtype == MUON_ROW_E5M2;
+  red_init(red);
+  int turn = 0;
+  for (int64_t blk = blockIdx.x; blk < a.batch * rb * cb; blk += gridDim.x) {
+    const int64_t j = blk % cb, i = blk / cb % rb, m = blk / (cb * rb);
+    const int64_t r0 = i * 128, c = j * 128 + cc;
+    const T* x = static_cast<const T*>(a.x) + m * a.x_matrix;
+    Chunk<T> v[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const int64_t r = r0 + rr + 16 * s;
+      if (r < a.rows) v[s].load(x + r * a.x_stride, c, a.cols);
+      else v[s] = Chunk<T>{};
+    }
+    float most = 0.f, f[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      v[s].settle(c, a.cols);
+      v[s].values(f);
+      most = fmaxf(most, most8(f));
+    }
+    const float scale = group_scale(group_max(most, red, turn), e5);
+    turn ^= 1;
+    if (t == 0) {
+      if (a.scales) a.scales[(m * rb + i) * cb + j] = scale;
+      if (a.scales_t) a.scales_t[(m * cb + j) * rb + i] = scale;
+    }
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const int lr = rr + 16 * s;
+      const int64_t r = r0 + lr;
+      v[s].values(f);
+      quotients8(f, scale);
+      if (a.q && r < a.rows) {
+        uint8_t* row = static_cast<uint8_t*>(a.q) + m * a.q_matrix + r * a.q_stride;
+        if (e5) store8_8bit<true>(row, c, a.cols, f);
+        else store8_8bit<false>(row, c, a.cols, f);
+      }
+      if (a.qt) {
+        if (e5) store8_8bit<true>(tile[lr], (int64_t)cc, (int64_t)128, f);
+        else store8_8bit<false>(tile[lr], (int64_t)cc, (int64_t)128, f);
+      }
+    }
+    if (a.qt) {
+      __syncthreads();
+      const int64_t n = a.rows - r0 < 128 ? a.rows - r0 : 128;
+      for (int e = t; e < 128 * 128; e += 256) {
+        const int lc = e >> 7, lr = e & 127;
+        if (j * 128 + lc < a.cols && lr < n)
+          static_cast<uint8_t*>(a.qt)[m * a.qt_matrix + (j * 128 + lc) * a.qt_stride + r0 + lr] = tile[lr][lc];
+      }
+      __syncthreads();
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t run_quantise(const muon_quantise_args& a, hipStream_t stream) {
+  const int64_t rb = (a.rows + 127) / 128, cb = (a.cols + 127) / 128, n = a.batch * rb * cb, most = 1 << 20;
+  const unsigned grid = unsigned(n < most ? n : most);
+  if (a.dtype == MUON_F32) ex_quantise<float><<<grid, 256, 0, stream>>>(a, rb, cb);
+  else ex_quantise<bf16_t><<<grid, 256, 0, stream>>>(a, rb, cb);
+  return hipGetLastError();
+}
+
+}  // namespace muon

@@ -57,9 +57,15 @@ template <> struct Chunk<bf16_t> {
   }
   template <class I>
   __device__ __forceinline__ void get(float* f, I c, I cols) {
-    if (c < cols && c + 8 > cols && cols >= 8) down((int)(c + 8 - cols));
-    unpack8(v, f);
+    settle(c, cols);
+    values(f);
   }
+  // get() in two: the shift once, the values as often as they are needed
+  template <class I>
+  __device__ __forceinline__ void settle(I c, I cols) {
+    if (c < cols && c + 8 > cols && cols >= 8) down((int)(c + 8 - cols));
+  }
+  __device__ __forceinline__ void values(float* f) const { unpack8(v, f); }
 };
 template <> struct Chunk<float> {
   u32x4 a, b;
@@ -101,7 +107,14 @@ template <> struct Chunk<float> {
   }
   template <class I>
   __device__ __forceinline__ void get(float* f, I c, I cols) {
+    settle(c, cols);
+    values(f);
+  }
+  template <class I>
+  __device__ __forceinline__ void settle(I c, I cols) {
     if (c < cols && c + 8 > cols && cols >= 8) down((int)(c + 8 - cols));
+  }
+  __device__ __forceinline__ void values(float* f) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       f[j] = __uint_as_float(a[j]);
@@ -173,6 +186,20 @@ __device__ __forceinline__ void store8(float* row, I c, I cols, const float* f) 
     }
     if (n & 1) *p = __uint_as_float(a[0]);
   }
+}
+
+// f / scale as fp32 divides (but for one in a million, an ulp off): 1 / scale
+// in two floats, the first a little too small so that the second is positive
+// and -0 keeps its sign.  2^-126 <= scale < 2^120, or infinite: then finite
+// elements become 0 and infinite ones NaN.  One multiplication more an
+// element than by the reciprocal alone, which moves a few in a million by an
+// 8-bit step: norm of [4096, 8192] to e4m3 45.6 us against 45.4, of
+// [32768, 1024] by groups of 32 24.2 against 23.6.
+__device__ __forceinline__ void quotients8(float* f, float scale) {
+  const float inv = __builtin_amdgcn_rcpf(scale) * (1.f - 0x1p-22f);
+  const float rest = scale < HUGE_VALF ? __builtin_fmaf(-scale, inv, 1.f) * inv : 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = __builtin_fmaf(f[j], inv, f[j] * rest);
 }
 
 // Eight values divided by their scale in an 8-bit format, rounded to nearest
