@@ -41,22 +41,35 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int experts, i
       const uint32_t o = __shfl_up(sum, d, WAVE);
       if (lane >= d) sum += o;
     }
-    const uint32_t total = __shfl(sum, WAVE - 1, WAVE);
+    const uint32_t total = __builtin_amdgcn_readlane(sum, WAVE - 1);
     if (index < before + total) {
       const unsigned long long past = __ballot(index < before + sum);
       const int at = __ffsll((long long)past) - 1;
-      const uint32_t own = __shfl(tm, at, WAVE), end = __shfl(sum, at, WAVE);
+      const uint32_t own = __builtin_amdgcn_readlane(tm, at), end = __builtin_amdgcn_readlane(sum, at);
       const uint32_t local = index - (before + end - own * tiles_n);
-      const int l = __shfl(lo, at, WAVE), h = __shfl(hi, at, WAVE);
-      t.e = __builtin_amdgcn_readfirstlane(e0 + at);
-      t.tn = __builtin_amdgcn_readfirstlane(local / own);
-      t.row0 = __builtin_amdgcn_readfirstlane(l + (int)(local % own) * bm);
-      t.rows = __builtin_amdgcn_readfirstlane(min(h - t.row0, bm));
+      const uint32_t n = __builtin_amdgcn_readfirstlane(local / own), m = local - n * own;
+      t.e = e0 + at;
+      t.tn = (int)n;
+      t.row0 = __builtin_amdgcn_readlane(lo, at) + (int)m * bm;
+      t.rows = min((int)__builtin_amdgcn_readlane(hi, at) - t.row0, bm);
       return true;
     }
     before += total;
   }
   return false;
+}
+
+// Tiles of the launch; every lane of a wave takes part.
+__device__ __forceinline__ uint32_t count_tiles(const int32_t* offsets, int experts, int rows, int bm, uint32_t tiles_n) {
+  uint32_t sum = 0;
+  for (int e = threadIdx.x & (WAVE - 1); e < experts; e += WAVE) {
+    int lo, hi;
+    run_of(offsets, e, rows, lo, hi);
+    sum += (uint32_t)(hi - lo + bm - 1) / (uint32_t)bm * tiles_n;
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, WAVE);
+  return __builtin_amdgcn_readfirstlane(sum);
 }
 
 // Bytes k .. k+15 of a row of K bytes, zeros from K on (k may lie past it).

@@ -1,6 +1,7 @@
 // The experts' 8-bit products (gfx950): out[i, n] = sum_b s_b sum_{k in b}
 // a[i, k] w[e, n, k] with a scale for each block of 128 of k.
 #include "experts_tiles.h"
+#include "lds.h"
 
 namespace muon {
 namespace {
@@ -165,8 +166,210 @@ ex_product(muon_product_args p, uint32_t tiles_n) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// 256 x 256 a workgroup of eight waves, 128 columns x 64 rows a wave, for 8-bit
+// rows of whole 16-byte pieces and at least two blocks.
+//
+// Both operands come straight from global memory into one of two stages of 128
+// bytes of each row.  A wave multiplies a stage in two halves of 64 columns: it
+// reads the fragments, then runs 16 instructions of 32 cycles with four
+// multiply-adds behind each, which scale its result and add it.  The waves form
+// two groups of four, one wave of each on a SIMD, and the second is a quarter
+// step behind: while one reads, the other multiplies.  A barrier ends each
+// quarter.  Block b's loads go to the stage of block b - 2, which both groups
+// have read when they start on block b - 1; each wave issues its share of them
+// before its first reads of b - 1 and waits for it as late as the other group's
+// order allows.
+// ---------------------------------------------------------------------------
+constexpr int kTile = 256, kStage = 2 * kTile * 128 + kTile * 4;
+
+// A tile's operands: its first rows, the rows' scales, and the last row of each.
+struct Operands {
+  const uint8_t* w;
+  const uint8_t* a;
+  const float* s;
+  int wl, al;
+};
+
+__device__ __forceinline__ u32x4 lds_read16(uint32_t at) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>((uintptr_t)at);
+}
+__device__ __forceinline__ float lds_read4(uint32_t at) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) float*>((uintptr_t)at);
+}
+// A value that every lane reads, through the scalar cache.
+__device__ __forceinline__ float uniform_load(const float* p) {
+  return *reinterpret_cast<const __attribute__((address_space(4))) float*>((uintptr_t)p);
+}
+
+template <int FW, int FA>
+__global__ void __launch_bounds__(512, 2)
+ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
+  typedef Block<FW, FA, bf16_t> Blk;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
+  __shared__ int32_t runs[MUON_ROUTE_MAX_EXPERTS + 1];
+  const int t = threadIdx.x, lane = t & 63, g = lane >> 4, q = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6), wn = w & 1, wm = (w >> 1) & 3;
+  const bool second = w >= 4;
+  const int E = (int)p.num_experts, rows = (int)p.rows, K = (int)p.k, KB = (K + 127) / 128;
+  const int NB = (int)((p.n + 127) / 128);
+  for (int e = t; e <= E; e += 512) runs[e] = p.offsets ? p.offsets[e] : e ? rows : 0;
+  __syncthreads();
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+
+  // consecutive tiles, which share their operands, to the workgroups of one XCD (every eighth)
+  const uint32_t total = count_tiles(runs, E, rows, kTile, tiles_n);
+  const uint32_t per = (total + 7) / 8, xcd = blockIdx.x & 7, step = gridDim.x >> 3;
+  const uint32_t end = min(total, xcd * per + per);
+  uint32_t index = xcd * per + (blockIdx.x >> 3);
+  ExpertTile tile;
+  if (index >= end || !find_tile(runs, E, rows, kTile, tiles_n, index, tile)) return;
+
+  auto operands = [&](const ExpertTile& x) {
+    const int64_t n0 = (int64_t)x.tn * kTile;
+    return Operands{static_cast<const uint8_t*>(p.w) + (int64_t)x.e * p.w_matrix + n0 * p.w_stride,
+                    static_cast<const uint8_t*>(p.a) + (int64_t)x.row0 * p.a_stride,
+                    p.a_scales + (int64_t)x.row0 * p.a_scales_stride,
+                    (int)min((int64_t)kTile, p.n - n0) - 1, x.rows - 1};
+  };
+  // Block kb of a tile to a stage: this wave's 32 rows of each operand, eight a load, 16-byte piece c
+  // of row r in slot slot_of(r, c).  Rows past the end repeat the last; pieces past the end take the
+  // row's first one and are cleared by settle().  The offsets are formed anew each time: registers
+  // are short.
+  auto piece = [&](int j) { return ((lane & 7) ^ ((4 * j + (lane >> 4)) & 7)) * 16; };
+  auto issue = [&](const Operands& o, int kb, uint32_t stage) {
+    const uint32_t to = stage + w * 4096;
+    int r0 = 32 * w + (lane >> 3);
+    asm volatile("" : "+v"(r0));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t c = kb * 128 + piece(j), at = c < (uint32_t)K ? c : 0u;
+      lds_dma16(o.w, __umul24(min(r0 + 8 * j, o.wl), (uint32_t)p.w_stride) + at, to + j * 1024);
+      lds_dma16(o.a, __umul24(min(r0 + 8 * j, o.al), (uint32_t)p.a_stride) + at, to + kTile * 128 + j * 1024);
+    }
+    if (w < 4)
+      lds_dma4(o.s + kb, __umul24(min(2 * (r0 & ~7) + lane, o.al), (uint32_t)p.a_scales_stride) * 4u,
+               stage + 2 * kTile * 128 + w * 256);
+  };
+  // this wave's loads have arrived, block kb's in the given stage
+  auto settle = [&](int kb, uint32_t stage) {
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    if (kb * 128 + 128 > K) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (kb * 128 + piece(j) >= K) {
+          u32x4* to = reinterpret_cast<u32x4*>(lds + (stage - lds0) + w * 4096 + lane * 16 + j * 1024);
+          to[0] = u32x4{};
+          to[kTile * 8] = u32x4{};
+        }
+    }
+  };
+
+  Operands cur = operands(tile);
+  uint32_t here = lds0, there = lds0 + kStage;
+  issue(cur, 0, here);
+  settle(0, here);
+  lds_barrier();
+  if (second) lds_barrier();
+  const uint32_t lo = q * 128 + slot_of(q, 2 * g) * 16, hi = q * 128 + slot_of(q, 2 * g + 1) * 16;
+  for (bool more = true; more;) {
+    ExpertTile next = tile;   // the last tile loads its own first block once more
+    index += step;
+    more = index < end && find_tile(runs, E, rows, kTile, tiles_n, index, next);
+    const Operands then = operands(next);
+    const int64_t n0 = (int64_t)tile.tn * kTile + wn * 128;   // this wave's 128 columns: one block of scales
+    const float* ws = p.w_scales + ((int64_t)tile.e * NB + min((int)(n0 >> 7), NB - 1)) * KB;
+    f32x4 acc[2][4][4] = {};
+    for (int kb = 0; kb < KB; ++kb) {
+      const bool last = kb + 1 == KB;
+      const int nb = last ? 0 : kb + 1;
+      issue(last ? then : cur, nb, there);
+      const float sw = uniform_load(ws + kb);
+      i32x8 fw[4], fa[4];
+      float s[4];
+      const uint32_t wlo = here + wn * 16384 + lo, whi = here + wn * 16384 + hi;
+      const uint32_t alo = here + kTile * 128 + wm * 8192 + lo, ahi = here + kTile * 128 + wm * 8192 + hi;
+      const uint32_t as = here + 2 * kTile * 128 + (wm * 64 + q) * 4;
+      auto read = [&](uint32_t l, uint32_t h) {
+        const u32x4 x = lds_read16(l), y = lds_read16(h);
+        return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
+      };
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (half == 0) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            fa[j] = read(alo + j * 2048, ahi + j * 2048);
+            s[j] = lds_read4(as + j * 64);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fw[i] = read(wlo + (4 * half + i) * 2048, whi + (4 * half + i) * 2048);
+        if (half == 1 && second) settle(nb, there);
+        lds_barrier();
+        __builtin_amdgcn_s_setprio(1);
+        if (half == 0) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[j] *= sw;
+        }
+        f32x4 d[3];
+#pragma unroll
+        for (int x = 0; x < 18; ++x) {   // the multiply-adds two instructions behind
+          if (x < 16) d[x % 3] = Blk::mfma(fw[x >> 2], fa[x & 3]);
+          __builtin_amdgcn_sched_barrier(0);
+          if (x >= 2) {
+            const int y = x - 2;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[half][y >> 2][y & 3][r] = __builtin_fmaf(d[y % 3][r], s[y & 3], acc[half][y >> 2][y & 3][r]);
+            asm volatile("" : "+v"(acc[half][y >> 2][y & 3]));   // here, not where the sums are used
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_s_setprio(0);
+        if (half == 1 && !second) settle(nb, there);
+        if (half == 1 && last) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = wm * 64 + j * 16 + q;
+            if (r >= tile.rows) continue;
+            bf16_t* row = static_cast<bf16_t*>(p.out) + (int64_t)(tile.row0 + r) * p.out_stride;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int64_t n = n0 + i * 16 + 4 * g;
+              if (n < p.n) store4<bf16_t>(row, n, p.n, acc[i >> 2][i & 3][j]);
+            }
+          }
+        }
+        lds_barrier();
+      }
+      const uint32_t x = here;
+      here = there;
+      there = x;
+    }
+    tile = next;
+    cur = then;
+  }
+  if (!second) lds_barrier();
+}
+
+// Rows in 16-byte pieces at 16-byte addresses, with a tile's offsets in 32 bits.
+bool whole_pieces(const muon_product_args& p) {
+  auto fine = [&](const void* base, int64_t stride) {
+    return reinterpret_cast<uintptr_t>(base) % 16 == 0 && stride % 16 == 0 && stride < (1 << 22);
+  };
+  return p.k % 16 == 0 && fine(p.a, p.rows > 1 ? p.a_stride : 0) && fine(p.w, p.n > 1 ? p.w_stride : 0) &&
+         (p.num_experts == 1 || p.w_matrix % 16 == 0) && p.a_scales_stride < (1 << 20) && p.k < (1 << 30);
+}
+
 template <int FW, int FA, typename O>
 hipError_t launch(const muon_product_args& p, hipStream_t stream) {
+  if constexpr (sizeof(O) == 2) {
+    if (whole_pieces(p) && p.k > 128) {
+      ex_product_tiled<FW, FA><<<256, 512, 0, stream>>>(p, (uint32_t)((p.n + kTile - 1) / kTile));
+      return hipGetLastError();
+    }
+  }
   const int64_t tiles_n = (p.n + 127) / 128;
   const int64_t most = (p.rows / 128 + (p.num_experts < p.rows ? p.num_experts : p.rows)) * tiles_n;
   ex_product<FW, FA, O><<<unsigned(most < (1 << 20) ? most : 1 << 20), 256, 0, stream>>>(p, (uint32_t)tiles_n);

@@ -1,20 +1,10 @@
 // The gradient of the experts' matrices (gfx950): dw[e] = dy_e^T x_e over the
 // expert's rows, bf16 products summed in fp32.
 #include "experts_tiles.h"
+#include "lds.h"
 
 namespace muon {
 namespace {
-
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-
-// ds_read_b64_tr_b16: within each 16-lane group, lane i receives element
-// i % 4 of the 4-element reads of lanes i / 4 + 4 q, q = 0..3.  With lane s
-// reading row k0 + s / 4 at columns c0 + 4 (s % 4) .. + 3, lane i gets column
-// c0 + i at rows k0 .. k0 + 3: a transposed 4 x 16 block.
-__device__ __forceinline__ bf16x4 lds_read_tr16(const bf16_t* p) {
-  typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
-  return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(__attribute__((address_space(3))) bf16_t*)p);
-}
 
 // Columns c .. c+7 of a bf16 row, zeros from `cols` on.
 __device__ __forceinline__ u32x4 load8_bf16(const bf16_t* row, int64_t c, int64_t cols) {
