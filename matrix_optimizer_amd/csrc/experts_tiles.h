@@ -34,7 +34,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int experts, i
     const int e = e0 + lane;
     int lo = 0, hi = 0;
     if (e < experts) run_of(offsets, e, rows, lo, hi);
-    const uint32_t tm = (uint32_t)(hi - lo + bm - 1) / (uint32_t)bm;
+    const uint32_t tm = ((uint32_t)(hi - lo) + bm - 1) / (uint32_t)bm;
     uint32_t sum = tm * tiles_n;
 #pragma unroll
     for (int d = 1; d < WAVE; d <<= 1) {
@@ -65,7 +65,7 @@ __device__ __forceinline__ uint32_t count_tiles(const int32_t* offsets, int expe
   for (int e = threadIdx.x & (WAVE - 1); e < experts; e += WAVE) {
     int lo, hi;
     run_of(offsets, e, rows, lo, hi);
-    sum += (uint32_t)(hi - lo + bm - 1) / (uint32_t)bm * tiles_n;
+    sum += ((uint32_t)(hi - lo) + bm - 1) / (uint32_t)bm * tiles_n;
   }
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, WAVE);

@@ -14,6 +14,12 @@ __device__ __forceinline__ bf16x4 lds_read_tr16(const bf16_t* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(__attribute__((address_space(3))) bf16_t*)p);
 }
 
+// The same at an LDS byte address.
+__device__ __forceinline__ bf16x4 lds_read_tr16_at(uint32_t at) {
+  typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4bf16(reinterpret_cast<lds_bf16x4*>((uintptr_t)at));
+}
+
 // A wave-uniform 64-bit value moved to scalar registers (the compiler
 // computes uniform divisions in vector registers; these stay live across a
 // tile's main loop).

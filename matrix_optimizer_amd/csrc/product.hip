@@ -167,8 +167,8 @@ ex_product(muon_product_args p, uint32_t tiles_n) {
 }
 
 // ---------------------------------------------------------------------------
-// 256 x 256 a workgroup of eight waves, 128 columns x 64 rows a wave, for 8-bit
-// rows of whole 16-byte pieces and at least two blocks.
+// 256 x 256 a workgroup of eight waves, 128 columns x 64 rows a wave, for
+// 8-bit rows of whole 16-byte pieces.
 //
 // Both operands come straight from global memory into one of two stages of 128
 // bytes of each row.  A wave multiplies a stage in two halves of 64 columns: it
@@ -359,13 +359,14 @@ bool whole_pieces(const muon_product_args& p) {
     return reinterpret_cast<uintptr_t>(base) % 16 == 0 && stride % 16 == 0 && stride < (1 << 22);
   };
   return p.k % 16 == 0 && fine(p.a, p.rows > 1 ? p.a_stride : 0) && fine(p.w, p.n > 1 ? p.w_stride : 0) &&
-         (p.num_experts == 1 || p.w_matrix % 16 == 0) && p.a_scales_stride < (1 << 20) && p.k < (1 << 30);
+         (p.num_experts == 1 || p.w_matrix % 16 == 0) && p.a_scales_stride < (1 << 20) && p.k < (1 << 30) &&
+         p.rows < (1 << 30);
 }
 
 template <int FW, int FA, typename O>
 hipError_t launch(const muon_product_args& p, hipStream_t stream) {
   if constexpr (sizeof(O) == 2) {
-    if (whole_pieces(p) && p.k > 128) {
+    if (whole_pieces(p)) {
       ex_product_tiled<FW, FA><<<256, 512, 0, stream>>>(p, (uint32_t)((p.n + kTile - 1) / kTile));
       return hipGetLastError();
     }

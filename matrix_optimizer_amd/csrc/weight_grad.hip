@@ -6,26 +6,47 @@
 namespace muon {
 namespace {
 
+// Where a launch writes: dw itself, or fp32 parts of it that weight_grad_join
+// adds up.
+struct Dest {
+  void* base;
+  int64_t stride, matrix, part;   // elements; part 0: one part
+  int parts;
+};
+
+// Rows of part `part` of `parts` of the run [lo, hi), in whole steps of `unit` rows.
+__device__ __forceinline__ void part_of(int part, int parts, int unit, int& lo, int& hi) {
+  const int64_t steps = (hi - lo + unit - 1) / unit;
+  const int first = lo;
+  lo = min(hi, first + (int)(steps * part / parts) * unit);
+  hi = min(hi, first + (int)(steps * (part + 1) / parts) * unit);
+}
+
 // Columns c .. c+7 of a bf16 row, zeros from `cols` on.
 __device__ __forceinline__ u32x4 load8_bf16(const bf16_t* row, int64_t c, int64_t cols) {
   return load16(reinterpret_cast<const uint8_t*>(row), c * 2, cols * 2);
 }
 
+// ---------------------------------------------------------------------------
 // 128 x 128 of one expert's matrix a workgroup, 64 x 64 a wave, 32 rows a
 // step: both operands lie with the rows of the sum along the slow axis, so
-// their fragments are read transposed.  Any size, stride and alignment.
+// their fragments are read transposed.  Any size, stride and alignment,
+// through registers.
+// ---------------------------------------------------------------------------
 template <typename O>
 __global__ void __launch_bounds__(256)
-ex_weight_grad(muon_weight_grad_args p, int64_t tn, int64_t tk) {
+ex_weight_grad(muon_weight_grad_args p, Dest d, int64_t tn, int64_t tk) {
   constexpr int BK = 32;
   __shared__ u32x4 lds[2][BK][16];   // rows of 128 columns of dy and of x
   const int t = threadIdx.x, lane = t & 63, w = t >> 6, wn = w & 1, wk = w >> 1;
-  for (int64_t index = blockIdx.x; index < p.num_experts * tn * tk; index += gridDim.x) {
-    const int64_t jk = index % tk, jn = index / tk % tn;
-    const int e = (int)(index / (tk * tn));
+  for (int64_t index = blockIdx.x; index < p.num_experts * tn * tk * d.parts; index += gridDim.x) {
+    const int part = (int)(index % d.parts);
+    const int64_t tile = index / d.parts, jk = tile % tk, jn = tile / tk % tn;
+    const int e = (int)(tile / (tk * tn));
     const int64_t n0 = jn * 128, k0 = jk * 128;
     int lo, hi;
     run_of(p.offsets, e, (int)p.rows, lo, hi);
+    part_of(part, d.parts, 64, lo, hi);
     f32x16 acc[2][2] = {};
     for (int64_t r0 = lo; r0 < hi; r0 += BK) {
       __syncthreads();
@@ -67,7 +88,7 @@ ex_weight_grad(muon_weight_grad_args p, int64_t tn, int64_t tk) {
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[0][i], f[1][j], acc[i][j], 0, 0, 0);
       }
     }
-    O* out = static_cast<O*>(p.dw) + e * p.dw_matrix;
+    O* out = static_cast<O*>(d.base) + part * d.part + e * d.matrix;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -75,20 +96,271 @@ ex_weight_grad(muon_weight_grad_args p, int64_t tn, int64_t tk) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int64_t n = n0 + wn * 64 + i * 32 + mfma32_row(lane, r), k = k0 + wk * 64 + j * 32 + mfma32_col(lane);
-          if (n < p.n && k < p.k) st_from_f32(out, n * p.dw_stride + k, acc[i][j][r]);
+          if (n < p.n && k < p.k) st_from_f32(out, n * d.stride + k, acc[i][j][r]);
         }
   }
 }
 
+// ---------------------------------------------------------------------------
+// 256 x 256 a workgroup of eight waves, 64 (n) x 128 (k) a wave, for rows of
+// whole 16-byte pieces.
+//
+// 64 rows of both operands at a time come straight from global memory into one
+// of two stages; a wave multiplies a stage in two halves of 32 rows, 16
+// instructions of 32 cycles each.  The waves form two groups, one wave of each
+// on a SIMD, the second a quarter step behind, so that one reads its fragments
+// (transposed, 48 registers) while the other multiplies; a barrier ends each
+// quarter.  A stage is loaded while the other is worked on: each wave issues its
+// share before its first reads and waits for it as late as the other group's
+// order allows.  x's columns are the instruction's rows, so that a lane ends with
+// runs of four along k, eight after one exchange with the lane 32 away.
+// ---------------------------------------------------------------------------
+constexpr int kTile = 256, kRows = 64, kStage = 2 * kRows * kTile * 2;
+
+// A tile's operands at its first columns, its run of rows and its place in the output.
+struct Tile {
+  const bf16_t* dy;
+  const bf16_t* x;
+  int lo, hi;
+  int e, part, n0, k0;
+};
+
+__device__ __forceinline__ bf16x8 read_tr(uint32_t at) {
+  const bf16x4 a = lds_read_tr16_at(at), b = lds_read_tr16_at(at + 4 * 512);
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+template <typename O>
+__device__ __forceinline__ void store_block(O* row, int64_t k0, int64_t K, const f32x16& v, int half, bool live);
+// Columns k0 .. k0+31 of a row, of which lanes below 32 hold runs of four at 8 q and the others at 8 q + 4.
+template <>
+__device__ __forceinline__ void store_block<float>(float* row, int64_t k0, int64_t K, const f32x16& v, int half, bool live) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t k = k0 + 8 * q + 4 * half;
+    if (live && k < K)   // K is a multiple of 8
+      *reinterpret_cast<u32x4_any*>(row + k) = u32x4{__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                                     __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])};
+  }
+}
+template <>
+__device__ __forceinline__ void store_block<bf16_t>(bf16_t* row, int64_t k0, int64_t K, const f32x16& v, int half, bool live) {
+#pragma unroll
+  for (int q = 0; q < 4; q += 2) {
+    // lanes below 32 keep run q and take its other half, the others run q + 1
+    const auto a = __builtin_amdgcn_permlane32_swap(pack_bf16(v[4 * q], v[4 * q + 1]), pack_bf16(v[4 * q + 4], v[4 * q + 5]),
+                                                    false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(pack_bf16(v[4 * q + 2], v[4 * q + 3]),
+                                                    pack_bf16(v[4 * q + 6], v[4 * q + 7]), false, false);
+    const int64_t k = k0 + 8 * (q + half);
+    if (live && k < K) *reinterpret_cast<u32x4_any*>(row + k) = u32x4{a[0], b[0], a[1], b[1]};
+  }
+}
+
+template <typename O>
+__global__ void __launch_bounds__(512, 2)
+ex_weight_grad_tiled(muon_weight_grad_args p, Dest d, uint32_t tn, uint32_t tk) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
+  const int t = threadIdx.x, lane = t & 63;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6), wk = w & 1, wn = (w >> 1) & 3;
+  const bool second = w >= 4;
+  const int rows = (int)p.rows;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+
+  // An expert's tiles, which share their operands, are dealt in eight runs to the XCDs (every eighth
+  // workgroup); few tiles an expert go round.
+  const uint32_t each = tn * tk * d.parts, xcd = blockIdx.x & 7;
+  const bool deal = each >= 64;
+  const uint32_t from = deal ? (uint32_t)((uint64_t)each * xcd / 8) : 0;
+  const uint32_t mine = deal ? (uint32_t)((uint64_t)each * (xcd + 1) / 8) - from : each;
+  const uint32_t total = mine * (uint32_t)p.num_experts, step = deal ? gridDim.x >> 3 : gridDim.x;
+  uint32_t index = deal ? blockIdx.x >> 3 : blockIdx.x;
+  if (index >= total) return;
+  auto tile_at = [&](uint32_t i) {
+    Tile x;
+    const uint32_t e = i / mine, local = from + i - e * mine, part = local % d.parts, u = local / d.parts;
+    x.e = (int)__builtin_amdgcn_readfirstlane(e);
+    x.part = (int)__builtin_amdgcn_readfirstlane(part);
+    x.n0 = (int)__builtin_amdgcn_readfirstlane(u / tk) * kTile;
+    x.k0 = (int)__builtin_amdgcn_readfirstlane(u % tk) * kTile;
+    int lo, hi;
+    run_of(p.offsets, x.e, rows, lo, hi);
+    part_of(x.part, d.parts, kRows, lo, hi);
+    x.lo = __builtin_amdgcn_readfirstlane(lo);
+    x.hi = __builtin_amdgcn_readfirstlane(hi);
+    x.dy = static_cast<const bf16_t*>(p.dy) + x.n0;
+    x.x = static_cast<const bf16_t*>(p.x) + x.k0;
+    return x;
+  };
+
+  // Rows first .. first + 63 to a stage: this wave's eight rows of each operand, two a load, 16-byte
+  // piece c of row r in slot c ^ 4 (r % 4), so that the four rows of a transposing read lie on different
+  // banks.  Rows past the run's end take some row and are cleared by settle(), columns past the matrix
+  // its tile's first ones.
+  const int piece[2] = {(lane & 31) ^ (4 * (lane >> 5)), (lane & 31) ^ (4 * (lane >> 5) + 8)};   // of rows 2 j + (lane >> 5), j even / odd
+  auto issue = [&](const Tile& x, int first, uint32_t stage) {
+    const int base = min(first, rows - 1);
+    const bf16_t* dy = x.dy + (int64_t)base * p.dy_stride;
+    const bf16_t* xx = x.x + (int64_t)base * p.x_stride;
+    const uint32_t to = stage + w * 4096;
+    int r0 = 8 * w + (lane >> 5);
+    asm volatile("" : "+v"(r0));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t r = min(r0 + 2 * j, rows - 1 - base), c = piece[j & 1] * 8;
+      lds_dma16(dy, (__umul24(r, (uint32_t)p.dy_stride) + (x.n0 + c < p.n ? c : 0u)) * 2, to + j * 1024);
+      lds_dma16(xx, (__umul24(r, (uint32_t)p.x_stride) + (x.k0 + c < p.k ? c : 0u)) * 2, to + kStage / 2 + j * 1024);
+    }
+  };
+  auto settle = [&](int first, int hi, uint32_t stage) {
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    if (first + kRows > hi) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (first + 8 * w + 2 * j + (lane >> 5) >= hi) {
+          u32x4* to = reinterpret_cast<u32x4*>(lds + (stage - lds0) + w * 4096 + lane * 16 + j * 1024);
+          to[0] = u32x4{};
+          to[kStage / 32] = u32x4{};
+        }
+    }
+  };
+
+  Tile cur = tile_at(index);
+  uint32_t here = lds0, there = lds0 + kStage;
+  issue(cur, cur.lo, here);
+  settle(cur.lo, cur.hi, here);
+  lds_barrier();
+  if (second) lds_barrier();
+  // Of 32 columns (block b of the operand's eight) a lane reads rows 8 (G / 2) + s / 4 and four below, columns
+  // 16 (G % 2) + 4 (s % 4) on, in 16-lane group G at lane s.
+  const int G = lane >> 4, s4 = lane & 15;
+  auto column = [&](int b) {
+    return (8 * (G >> 1) + (s4 >> 2)) * 512 + (((4 * b + 2 * (G & 1) + ((s4 & 3) >> 1)) ^ (4 * (s4 >> 2))) * 16) + (s4 & 1) * 8;
+  };
+  uint32_t xa[4], da[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) xa[i] = column(4 * wk + i) + kStage / 2;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) da[j] = column(2 * wn + j);
+
+  for (bool more = true; more;) {
+    index += step;
+    more = index < total;
+    const Tile next = more ? tile_at(index) : cur;   // the last tile loads its own first rows once more
+    f32x16 acc[4][2] = {};
+    for (int first = cur.lo, last = 0; !last; first += kRows) {
+      last = first + kRows >= cur.hi;
+      const Tile& of = last ? next : cur;
+      const int nf = last ? next.lo : first + kRows, nh = last ? next.hi : cur.hi;
+      issue(of, nf, there);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        bf16x8 fx[2][4], fd[2][2];
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) fx[kk][i] = read_tr(here + xa[i] + (2 * half + kk) * 16 * 512);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) fd[kk][j] = read_tr(here + da[j] + (2 * half + kk) * 16 * 512);
+        }
+        if (half == 1 && second) settle(nf, nh, there);
+        lds_barrier();
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fx[kk][i], fd[kk][j], acc[i][j], 0, 0, 0);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+        __builtin_amdgcn_s_setprio(0);
+        if (half == 1 && !second) settle(nf, nh, there);
+        if (half == 1 && last) {
+          O* out = static_cast<O*>(d.base) + cur.part * d.part + cur.e * d.matrix;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int64_t n = cur.n0 + wn * 64 + j * 32 + (lane & 31);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              store_block<O>(out + n * d.stride, cur.k0 + wk * 128 + i * 32, p.k, acc[i][j], lane >> 5, n < p.n);
+          }
+        }
+        lds_barrier();
+      }
+      const uint32_t x = here;
+      here = there;
+      there = x;
+    }
+    cur = next;
+  }
+  if (!second) lds_barrier();
+}
+
+// dw = the sum of the parts, in their order.
+template <typename O>
+__global__ void __launch_bounds__(256)
+ex_weight_grad_join(muon_weight_grad_args p, const float* parts, int n_parts, int64_t part) {
+  const int64_t chunks = (p.k + 7) / 8, all = p.num_experts * p.n * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / chunks, c = (i - row * chunks) * 8, e = row / p.n, n = row - e * p.n;
+    float s[8], f[8];
+    load8(parts + row * p.k, c, p.k, s);
+    for (int j = 1; j < n_parts; ++j) {
+      load8(parts + j * part + row * p.k, c, p.k, f);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s[q] += f[q];
+    }
+    store8(static_cast<O*>(p.dw) + e * p.dw_matrix + n * p.dw_stride, c, p.k, s);
+  }
+}
+
+bool whole_pieces(const muon_weight_grad_args& p) {
+  auto fine = [&](const void* base, int64_t stride, int64_t cols) {
+    return reinterpret_cast<uintptr_t>(base) % 16 == 0 && cols % 8 == 0 && (p.rows <= 1 || stride % 8 == 0) && stride < (1 << 22);
+  };
+  // a tile's row and column numbers fit 32 bits with room for the tile
+  return p.rows > 0 && p.rows < (1 << 30) && p.n < (1 << 30) && p.k < (1 << 30) && fine(p.dy, p.dy_stride, p.n) &&
+         fine(p.x, p.x_stride, p.k);
+}
+
+template <typename O>
+hipError_t launch(const muon_weight_grad_args& p, const Dest& d, hipStream_t stream) {
+  const int64_t tn = (p.n + kTile - 1) / kTile, tk = (p.k + kTile - 1) / kTile;
+  if (whole_pieces(p) && p.num_experts * tn * tk * d.parts < (int64_t(1) << 31)) {
+    ex_weight_grad_tiled<O><<<256, 512, 0, stream>>>(p, d, (uint32_t)tn, (uint32_t)tk);
+  } else {
+    const int64_t sn = (p.n + 127) / 128, sk = (p.k + 127) / 128, tiles = p.num_experts * sn * sk * d.parts;
+    ex_weight_grad<O><<<unsigned(tiles < (1 << 20) ? tiles : 1 << 20), 256, 0, stream>>>(p, d, sn, sk);
+  }
+  return hipGetLastError();
+}
+
 }  // namespace
 
-int64_t weight_grad_parts(int64_t, int64_t, int64_t, int64_t) { return 1; }
+// Few tiles and many rows: the rows are split so that there are tiles for the 256 CUs, with 512 rows of
+// the mean expert a part at least (eight stages, against one write and one read of the part).
+int64_t weight_grad_parts(int64_t rows, int64_t num_experts, int64_t n, int64_t k) {
+  const int64_t tiles = num_experts * ((n + kTile - 1) / kTile) * ((k + kTile - 1) / kTile);
+  const int64_t want = 256 / tiles, most = rows / num_experts / 512;
+  const int64_t parts = want < most ? want : most;
+  return parts < 2 ? 1 : parts;
+}
 
-hipError_t run_weight_grad(const muon_weight_grad_args& p, float*, hipStream_t stream) {
-  const int64_t tn = (p.n + 127) / 128, tk = (p.k + 127) / 128, tiles = p.num_experts * tn * tk;
-  const unsigned grid = unsigned(tiles < (1 << 20) ? tiles : 1 << 20);
-  if (p.dw_dtype == MUON_F32) ex_weight_grad<float><<<grid, 256, 0, stream>>>(p, tn, tk);
-  else ex_weight_grad<bf16_t><<<grid, 256, 0, stream>>>(p, tn, tk);
+hipError_t run_weight_grad(const muon_weight_grad_args& p, float* parts, hipStream_t stream) {
+  const int64_t n_parts = weight_grad_parts(p.rows, p.num_experts, p.n, p.k), part = p.num_experts * p.n * p.k;
+  const bool f32 = p.dw_dtype == MUON_F32;
+  if (n_parts == 1) {
+    const Dest d{p.dw, p.dw_stride, p.dw_matrix, 0, 1};
+    return f32 ? launch<float>(p, d, stream) : launch<bf16_t>(p, d, stream);
+  }
+  const hipError_t err = launch<float>(p, Dest{parts, p.k, p.n * p.k, part, (int)n_parts}, stream);
+  if (err != hipSuccess) return err;
+  const int64_t blocks = (p.num_experts * p.n * ((p.k + 7) / 8) + 255) / 256;
+  const unsigned grid = unsigned(blocks < (1 << 16) ? blocks : 1 << 16);
+  if (f32) ex_weight_grad_join<float><<<grid, 256, 0, stream>>>(p, parts, (int)n_parts, part);
+  else ex_weight_grad_join<bf16_t><<<grid, 256, 0, stream>>>(p, parts, (int)n_parts, part);
   return hipGetLastError();
 }
 
