@@ -64,12 +64,14 @@ struct Block<FW, FA, float> {
   }
 };
 
-// Slot of 16-byte chunk c of a 128-byte row r: the 16 rows that a fragment
-// read touches at once lie on different banks.
+// Slot of 16-byte chunk c of a 128-byte row r.  A 16-byte read is served for
+// lanes 0-3, 12-15 and 20-27 at once, then for the others of the 32, and so on:
+// with chunks g and g + 4 for lane group g they lie on different banks (2 g and
+// 2 g + 1 had half of the reads wait, and the large product 1.80 ms).
 __device__ __forceinline__ int slot_of(int r, int c) { return c ^ ((r >> 1) & 7); }
 
 __device__ __forceinline__ i32x8 fragment(const u32x4* rows, int r, int g) {
-  const u32x4 lo = rows[r * 8 + slot_of(r, 2 * g)], hi = rows[r * 8 + slot_of(r, 2 * g + 1)];
+  const u32x4 lo = rows[r * 8 + slot_of(r, g)], hi = rows[r * 8 + slot_of(r, g + 4)];
   return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
@@ -168,27 +170,27 @@ ex_product(muon_product_args p, uint32_t tiles_n) {
 
 // ---------------------------------------------------------------------------
 // 256 x 256 a workgroup of eight waves, 128 columns x 64 rows a wave, for
-// 8-bit rows of whole 16-byte pieces.
+// 8-bit rows of whole 16-byte pieces and at least two blocks.
 //
 // Both operands come straight from global memory into one of two stages of 128
-// bytes of each row.  A wave multiplies a stage in two halves of 64 columns: it
-// reads the fragments, then runs 16 instructions of 32 cycles with four
-// multiply-adds behind each, which scale its result and add it.  The waves form
-// two groups of four, one wave of each on a SIMD, and the second is a quarter
-// step behind: while one reads, the other multiplies.  A barrier ends each
-// quarter.  Block b's loads go to the stage of block b - 2, which both groups
-// have read when they start on block b - 1; each wave issues its share of them
-// before its first reads of b - 1 and waits for it as late as the other group's
-// order allows.
+// bytes of each row.  A wave runs a block as 32 instructions of 32 cycles, in
+// four parts of two of its eight column fragments by its four row fragments;
+// behind each come the four multiply-adds that scale and add the result of the
+// one two before, and the reads of the next part's fragments.  The one barrier of
+// a block stands before its last part: then every wave has read the stage, so
+// block k + 2 may be loaded into it, and every wave's loads of block k + 1, a
+// whole block old, are there, so that the last part reads the first fragments of
+// the next block and no wave finds itself without operands.
 // ---------------------------------------------------------------------------
-constexpr int kTile = 256, kStage = 2 * kTile * 128 + kTile * 4;
+constexpr int kTile = 256, kStage = 2 * kTile * 128 + kTile * 4 + 256;
 
-// A tile's operands: its first rows, the rows' scales, and the last row of each.
+// A tile's operands: its first rows, the scales of its rows and columns, and the last row of each.
 struct Operands {
   const uint8_t* w;
   const uint8_t* a;
-  const float* s;
-  int wl, al;
+  const float* as;
+  const float* ws;
+  int wl, al, wb;   // wb: the second column block, or the first again
 };
 
 __device__ __forceinline__ u32x4 lds_read16(uint32_t at) {
@@ -197,20 +199,13 @@ __device__ __forceinline__ u32x4 lds_read16(uint32_t at) {
 __device__ __forceinline__ float lds_read4(uint32_t at) {
   return *reinterpret_cast<const __attribute__((address_space(3))) float*>((uintptr_t)at);
 }
-// A value that every lane reads, through the scalar cache.
-__device__ __forceinline__ float uniform_load(const float* p) {
-  return *reinterpret_cast<const __attribute__((address_space(4))) float*>((uintptr_t)p);
-}
-
 template <int FW, int FA>
 __global__ void __launch_bounds__(512, 2)
 ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
-  typedef Block<FW, FA, bf16_t> Blk;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
   __shared__ int32_t runs[MUON_ROUTE_MAX_EXPERTS + 1];
   const int t = threadIdx.x, lane = t & 63, g = lane >> 4, q = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6), wn = w & 1, wm = (w >> 1) & 3;
-  const bool second = w >= 4;
   const int E = (int)p.num_experts, rows = (int)p.rows, K = (int)p.k, KB = (K + 127) / 128;
   const int NB = (int)((p.n + 127) / 128);
   for (int e = t; e <= E; e += 512) runs[e] = p.offsets ? p.offsets[e] : e ? rows : 0;
@@ -229,27 +224,28 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
     const int64_t n0 = (int64_t)x.tn * kTile;
     return Operands{static_cast<const uint8_t*>(p.w) + (int64_t)x.e * p.w_matrix + n0 * p.w_stride,
                     static_cast<const uint8_t*>(p.a) + (int64_t)x.row0 * p.a_stride,
-                    p.a_scales + (int64_t)x.row0 * p.a_scales_stride,
-                    (int)min((int64_t)kTile, p.n - n0) - 1, x.rows - 1};
+                    p.a_scales + (int64_t)x.row0 * p.a_scales_stride, p.w_scales + ((int64_t)x.e * NB + 2 * x.tn) * KB,
+                    (int)min((int64_t)kTile, p.n - n0) - 1, x.rows - 1, 2 * x.tn + 1 < NB ? 1 : 0};
   };
-  // Block kb of a tile to a stage: this wave's 32 rows of each operand, eight a load, 16-byte piece c
-  // of row r in slot slot_of(r, c).  Rows past the end repeat the last; pieces past the end take the
-  // row's first one and are cleared by settle().  The offsets are formed anew each time: registers
-  // are short.
+  // Block kb of a tile to a stage, load `part` of nine: this wave's 32 rows of each operand, eight a
+  // load, 16-byte piece c of row r in slot slot_of(r, c), then scales.  Rows past the end repeat the
+  // last; pieces past the end take the row's first one and are cleared by settle().  The offsets are
+  // formed anew each time: registers are short.
   auto piece = [&](int j) { return ((lane & 7) ^ ((4 * j + (lane >> 4)) & 7)) * 16; };
-  auto issue = [&](const Operands& o, int kb, uint32_t stage) {
-    const uint32_t to = stage + w * 4096;
+  auto issue = [&](const Operands& o, int kb, uint32_t stage, int part) {
     int r0 = 32 * w + (lane >> 3);
     asm volatile("" : "+v"(r0));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t c = kb * 128 + piece(j), at = c < (uint32_t)K ? c : 0u;
-      lds_dma16(o.w, __umul24(min(r0 + 8 * j, o.wl), (uint32_t)p.w_stride) + at, to + j * 1024);
-      lds_dma16(o.a, __umul24(min(r0 + 8 * j, o.al), (uint32_t)p.a_stride) + at, to + kTile * 128 + j * 1024);
-    }
-    if (w < 4)
-      lds_dma4(o.s + kb, __umul24(min(2 * (r0 & ~7) + lane, o.al), (uint32_t)p.a_scales_stride) * 4u,
+    if (part < 8) {
+      const int j = part >> 1;
+      const uint32_t to = stage + w * 4096 + j * 1024, c = kb * 128 + piece(j), at = c < (uint32_t)K ? c : 0u;
+      if (part & 1) lds_dma16(o.a, __umul24(min(r0 + 8 * j, o.al), (uint32_t)p.a_stride) + at, to + kTile * 128);
+      else lds_dma16(o.w, __umul24(min(r0 + 8 * j, o.wl), (uint32_t)p.w_stride) + at, to);
+    } else if (w < 4) {
+      lds_dma4(o.as + kb, __umul24(min(2 * (r0 & ~7) + lane, o.al), (uint32_t)p.a_scales_stride) * 4u,
                stage + 2 * kTile * 128 + w * 256);
+    } else if (w == 4) {
+      lds_dma4(o.ws + kb, (uint32_t)(lane & o.wb) * (uint32_t)KB * 4u, stage + 2 * kTile * 128 + kTile * 4);
+    }
   };
   // this wave's loads have arrived, block kb's in the given stage
   auto settle = [&](int kb, uint32_t stage) {
@@ -264,93 +260,101 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
         }
     }
   };
+  auto read = [&](uint32_t l, uint32_t h) {
+    const u32x4 x = lds_read16(l), y = lds_read16(h);
+    return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
+  };
 
   Operands cur = operands(tile);
   uint32_t here = lds0, there = lds0 + kStage;
-  issue(cur, 0, here);
+#pragma unroll
+  for (int x = 0; x < 9; ++x) issue(cur, 0, here, x);
+#pragma unroll
+  for (int x = 0; x < 9; ++x) issue(cur, 1, there, x);
   settle(0, here);
   lds_barrier();
-  if (second) lds_barrier();
-  const uint32_t lo = q * 128 + slot_of(q, 2 * g) * 16, hi = q * 128 + slot_of(q, 2 * g + 1) * 16;
+  // this lane's addresses in a stage
+  const uint32_t lo = q * 128 + slot_of(q, g) * 16, hi = q * 128 + slot_of(q, g + 4) * 16;
+  const uint32_t wlo = wn * 16384 + lo, whi = wn * 16384 + hi;
+  const uint32_t alo = kTile * 128 + wm * 8192 + lo, ahi = kTile * 128 + wm * 8192 + hi;
+  const uint32_t sat = 2 * kTile * 128 + (wm * 64 + q) * 4, swat = 2 * kTile * 128 + kTile * 4 + wn * 4;
+  i32x8 fw[2][2], fa[4];
+  float sn[4], swn;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    fa[j] = read(here + alo + j * 2048, here + ahi + j * 2048);
+    sn[j] = lds_read4(here + sat + j * 64);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) fw[0][i] = read(here + wlo + i * 2048, here + whi + i * 2048);
+  swn = lds_read4(here + swat);
+
   for (bool more = true; more;) {
-    ExpertTile next = tile;   // the last tile loads its own first block once more
+    ExpertTile next = tile;   // the last tile loads its own first blocks once more
     index += step;
     more = index < end && find_tile(runs, E, rows, kTile, tiles_n, index, next);
     const Operands then = operands(next);
-    const int64_t n0 = (int64_t)tile.tn * kTile + wn * 128;   // this wave's 128 columns: one block of scales
-    const float* ws = p.w_scales + ((int64_t)tile.e * NB + min((int)(n0 >> 7), NB - 1)) * KB;
-    f32x4 acc[2][4][4] = {};
+    f32x4 acc[8][4] = {};
     for (int kb = 0; kb < KB; ++kb) {
-      const bool last = kb + 1 == KB;
-      const int nb = last ? 0 : kb + 1;
-      issue(last ? then : cur, nb, there);
-      const float sw = uniform_load(ws + kb);
-      i32x8 fw[4], fa[4];
+      const bool ahead = kb + 2 < KB;
+      const int nb = ahead ? kb + 2 : kb + 2 - KB;
+      const Operands& of = ahead ? cur : then;
       float s[4];
-      const uint32_t wlo = here + wn * 16384 + lo, whi = here + wn * 16384 + hi;
-      const uint32_t alo = here + kTile * 128 + wm * 8192 + lo, ahi = here + kTile * 128 + wm * 8192 + hi;
-      const uint32_t as = here + 2 * kTile * 128 + (wm * 64 + q) * 4;
-      auto read = [&](uint32_t l, uint32_t h) {
-        const u32x4 x = lds_read16(l), y = lds_read16(h);
-        return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
-      };
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (half == 0) {
+      for (int j = 0; j < 4; ++j) s[j] = sn[j] * swn;
+      f32x4 d[3];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            fa[j] = read(alo + j * 2048, ahi + j * 2048);
-            s[j] = lds_read4(as + j * 64);
+      for (int x = 0; x < 34; ++x) {
+        const int part = x >> 3, i = 2 * part + (x & 1), j = (x >> 1) & 3;
+        if (x == 24) {   // the stage is read, the next one is there
+          settle(kb + 1 < KB ? kb + 1 : 0, there);
+          lds_barrier();
+        }
+        if (x < 32) d[x % 3] = Block<FW, FA, bf16_t>::mfma(fw[part & 1][x & 1], fa[j]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (x >= 2) {
+          const int y = x - 2, yi = 2 * (y >> 3) + (y & 1), yj = (y >> 1) & 3;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[yi][yj][r] = __builtin_fmaf(d[y % 3][r], s[yj], acc[yi][yj][r]);
+          asm volatile("" : "+v"(acc[yi][yj]));   // here, not where the sums are used
+        }
+        if (x < 24) {
+          if ((x & 7) < 2) {
+            const int f = 2 * (part + 1) + (x & 7);
+            fw[(part + 1) & 1][x & 7] = read(here + wlo + f * 2048, here + whi + f * 2048);
           }
+        } else if (x < 32) {
+          if (x < 26) fw[0][x - 24] = read(there + wlo + (x - 24) * 2048, there + whi + (x - 24) * 2048);
+          if (x & 1) fa[j] = read(there + alo + j * 2048, there + ahi + j * 2048);
+          else sn[j] = lds_read4(there + sat + j * 64);
+          issue(of, nb, here, x - 24);
+        } else if (x == 32) {
+          swn = lds_read4(there + swat);
+          issue(of, nb, here, 8);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) fw[i] = read(wlo + (4 * half + i) * 2048, whi + (4 * half + i) * 2048);
-        if (half == 1 && second) settle(nb, there);
-        lds_barrier();
-        __builtin_amdgcn_s_setprio(1);
-        if (half == 0) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[j] *= sw;
-        }
-        f32x4 d[3];
-#pragma unroll
-        for (int x = 0; x < 18; ++x) {   // the multiply-adds two instructions behind
-          if (x < 16) d[x % 3] = Blk::mfma(fw[x >> 2], fa[x & 3]);
-          __builtin_amdgcn_sched_barrier(0);
-          if (x >= 2) {
-            const int y = x - 2;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              acc[half][y >> 2][y & 3][r] = __builtin_fmaf(d[y % 3][r], s[y & 3], acc[half][y >> 2][y & 3][r]);
-            asm volatile("" : "+v"(acc[half][y >> 2][y & 3]));   // here, not where the sums are used
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        __builtin_amdgcn_s_setprio(0);
-        if (half == 1 && !second) settle(nb, there);
-        if (half == 1 && last) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int r = wm * 64 + j * 16 + q;
-            if (r >= tile.rows) continue;
-            bf16_t* row = static_cast<bf16_t*>(p.out) + (int64_t)(tile.row0 + r) * p.out_stride;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int64_t n = n0 + i * 16 + 4 * g;
-              if (n < p.n) store4<bf16_t>(row, n, p.n, acc[i >> 2][i & 3][j]);
-            }
-          }
-        }
-        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
       }
       const uint32_t x = here;
       here = there;
       there = x;
     }
+    const int64_t n0 = (int64_t)tile.tn * kTile + wn * 128;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = wm * 64 + j * 16 + q;
+      if (r >= tile.rows) continue;
+      bf16_t* row = static_cast<bf16_t*>(p.out) + (int64_t)(tile.row0 + r) * p.out_stride;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t n = n0 + i * 16 + 4 * g;
+        if (n < p.n) store4<bf16_t>(row, n, p.n, acc[i][j]);
+      }
+    }
     tile = next;
     cur = then;
   }
-  if (!second) lds_barrier();
+  // the loads that are still on their way go to this workgroup's memory
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
 }
 
 // Rows in 16-byte pieces at 16-byte addresses, with a tile's offsets in 32 bits.
@@ -366,7 +370,7 @@ bool whole_pieces(const muon_product_args& p) {
 template <int FW, int FA, typename O>
 hipError_t launch(const muon_product_args& p, hipStream_t stream) {
   if constexpr (sizeof(O) == 2) {
-    if (whole_pieces(p)) {
+    if (whole_pieces(p) && p.k > 128) {
       ex_product_tiled<FW, FA><<<256, 512, 0, stream>>>(p, (uint32_t)((p.n + kTile - 1) / kTile));
       return hipGetLastError();
     }
