@@ -184,13 +184,11 @@ ex_product(muon_product_args p, uint32_t tiles_n) {
 // ---------------------------------------------------------------------------
 constexpr int kTile = 256, kStage = 2 * kTile * 128 + kTile * 4 + 256;
 
-// A tile's operands: its first rows, the scales of its rows and columns, and the last row of each.
+// A tile's operands as buffers that end with its last row: matrix and rows, the rows' scales, and the
+// columns' (those of two blocks, or of one and wb = 0).
 struct Operands {
-  const uint8_t* w;
-  const uint8_t* a;
-  const float* as;
-  const float* ws;
-  int wl, al, wb;   // wb: the second column block, or the first again
+  u32x4 w, a, as, ws;
+  int wb;
 };
 
 __device__ __forceinline__ u32x4 lds_read16(uint32_t at) {
@@ -220,31 +218,33 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
   ExpertTile tile;
   if (index >= end || !find_tile(runs, E, rows, kTile, tiles_n, index, tile)) return;
 
+  const uint32_t w_pitch = (uint32_t)p.w_stride, a_pitch = (uint32_t)p.a_stride, s_pitch = (uint32_t)p.a_scales_stride * 4u;
   auto operands = [&](const ExpertTile& x) {
     const int64_t n0 = (int64_t)x.tn * kTile;
-    return Operands{static_cast<const uint8_t*>(p.w) + (int64_t)x.e * p.w_matrix + n0 * p.w_stride,
-                    static_cast<const uint8_t*>(p.a) + (int64_t)x.row0 * p.a_stride,
-                    p.a_scales + (int64_t)x.row0 * p.a_scales_stride, p.w_scales + ((int64_t)x.e * NB + 2 * x.tn) * KB,
-                    (int)min((int64_t)kTile, p.n - n0) - 1, x.rows - 1, 2 * x.tn + 1 < NB ? 1 : 0};
+    const int wl = (int)min((int64_t)kTile, p.n - n0) - 1, al = x.rows - 1, wb = 2 * x.tn + 1 < NB ? 1 : 0;
+    return Operands{buffer_of(static_cast<const uint8_t*>(p.w) + (int64_t)x.e * p.w_matrix + n0 * p.w_stride, wl * w_pitch + K),
+                    buffer_of(static_cast<const uint8_t*>(p.a) + (int64_t)x.row0 * p.a_stride, al * a_pitch + K),
+                    buffer_of(p.a_scales + (int64_t)x.row0 * p.a_scales_stride, al * s_pitch + KB * 4),
+                    buffer_of(p.w_scales + ((int64_t)x.e * NB + 2 * x.tn) * KB, (wb + 1) * KB * 4), wb};
   };
   // Block kb of a tile to a stage, load `part` of nine: this wave's 32 rows of each operand, eight a
-  // load, 16-byte piece c of row r in slot slot_of(r, c), then scales.  Rows past the end repeat the
-  // last; pieces past the end take the row's first one and are cleared by settle().  The offsets are
-  // formed anew each time: registers are short.
+  // load, 16-byte piece c of row r in slot slot_of(r, c), then scales.  Pieces past the end of a row are
+  // cleared by settle().
   auto piece = [&](int j) { return ((lane & 7) ^ ((4 * j + (lane >> 4)) & 7)) * 16; };
+  const uint32_t row = 32 * w + (lane >> 3);
+  const uint32_t w_off[2] = {row * w_pitch + piece(0), row * w_pitch + piece(1)};
+  const uint32_t a_off[2] = {row * a_pitch + piece(0), row * a_pitch + piece(1)};
+  const uint32_t s_off = w < 4 ? (64 * w + lane) * s_pitch : (lane & 1) * KB * 4;
   auto issue = [&](const Operands& o, int kb, uint32_t stage, int part) {
-    int r0 = 32 * w + (lane >> 3);
-    asm volatile("" : "+v"(r0));
     if (part < 8) {
       const int j = part >> 1;
-      const uint32_t to = stage + w * 4096 + j * 1024, c = kb * 128 + piece(j), at = c < (uint32_t)K ? c : 0u;
-      if (part & 1) lds_dma16(o.a, __umul24(min(r0 + 8 * j, o.al), (uint32_t)p.a_stride) + at, to + kTile * 128);
-      else lds_dma16(o.w, __umul24(min(r0 + 8 * j, o.wl), (uint32_t)p.w_stride) + at, to);
+      const uint32_t to = stage + w * 4096 + j * 1024;
+      if (part & 1) lds_dma16(o.a, a_off[j & 1], kb * 128 + 8 * j * a_pitch, to + kTile * 128);
+      else lds_dma16(o.w, w_off[j & 1], kb * 128 + 8 * j * w_pitch, to);
     } else if (w < 4) {
-      lds_dma4(o.as + kb, __umul24(min(2 * (r0 & ~7) + lane, o.al), (uint32_t)p.a_scales_stride) * 4u,
-               stage + 2 * kTile * 128 + w * 256);
+      lds_dma4(o.as, s_off, kb * 4, stage + 2 * kTile * 128 + w * 256);
     } else if (w == 4) {
-      lds_dma4(o.ws + kb, (uint32_t)(lane & o.wb) * (uint32_t)KB * 4u, stage + 2 * kTile * 128 + kTile * 4);
+      lds_dma4(o.ws, o.wb ? s_off : 0u, kb * 4, stage + 2 * kTile * 128 + kTile * 4);
     }
   };
   // this wave's loads have arrived, block kb's in the given stage
