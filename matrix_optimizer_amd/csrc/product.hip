@@ -168,6 +168,17 @@ ex_product(muon_product_args p, uint32_t tiles_n) {
   }
 }
 
+// Eight columns of a bf16 row, of which `left` belong to it.
+__device__ __forceinline__ void store_packed8(bf16_t* p, int left, const u32x4& v) {
+  if (left >= 8) {
+    *reinterpret_cast<u32x4_any*>(p) = v;
+  } else {
+#pragma unroll
+    for (int r = 0; r < 7; ++r)
+      if (r < left) p[r] = (bf16_t)(v[r >> 1] >> (16 * (r & 1)));
+  }
+}
+
 // ---------------------------------------------------------------------------
 // 256 x 256 a workgroup of eight waves, 128 columns x 64 rows a wave, for
 // 8-bit rows of whole 16-byte pieces and at least two blocks.
@@ -248,8 +259,11 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
     }
   };
   // this wave's loads have arrived, block kb's in the given stage
+  bool stores = false;
   auto settle = [&](int kb, uint32_t stage) {
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    if (stores) __builtin_amdgcn_s_waitcnt(vmcnt_imm(16));   // counted in the order of issue
+    else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    stores = false;
     if (kb * 128 + 128 > K) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -339,17 +353,27 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
       there = x;
     }
     const int64_t n0 = (int64_t)tile.tn * kTile + wn * 128;
+    bf16_t* out = static_cast<bf16_t*>(p.out) + (int64_t)(tile.row0 + wm * 64) * p.out_stride + n0;
+    const int n_left = (int)min((int64_t)128, p.n - n0), r_left = tile.rows - wm * 64;
+    int lq = lane;   // formed here: registers are short in the loop
+    asm volatile("" : "+v"(lq));
+    const int c0 = ((lq >> 4) & 1) * 16 + (lq >> 5) * 8;
+    lq &= 15;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int r = wm * 64 + j * 16 + q;
-      if (r >= tile.rows) continue;
-      bf16_t* row = static_cast<bf16_t*>(p.out) + (int64_t)(tile.row0 + r) * p.out_stride;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t n = n0 + i * 16 + 4 * g;
-        if (n < p.n) store4<bf16_t>(row, n, p.n, acc[i][j]);
+      for (int i = 0; i < 8; i += 2) {
+        // lane groups 0 and 2 take the fragment's other four columns from 1 and 3, which take theirs of the next
+        const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16(acc[i][j][0], acc[i][j][1]),
+                                                        pack_bf16(acc[i + 1][j][0], acc[i + 1][j][1]), false, false);
+        const auto y = __builtin_amdgcn_permlane16_swap(pack_bf16(acc[i][j][2], acc[i][j][3]),
+                                                        pack_bf16(acc[i + 1][j][2], acc[i + 1][j][3]), false, false);
+        const int r = j * 16 + lq, n = i * 16 + c0;
+        if (r < r_left) store_packed8(out + (__umul24(r, (uint32_t)p.out_stride) + n), n_left - n, u32x4{x[0], y[0], x[1], y[1]});
       }
     }
+    // sixteen stores, and nothing else, behind the loads that settle() waits for next
+    stores = n_left == 128 && r_left >= 64;
     tile = next;
     cur = then;
   }
@@ -364,7 +388,7 @@ bool whole_pieces(const muon_product_args& p) {
   };
   return p.k % 16 == 0 && fine(p.a, p.rows > 1 ? p.a_stride : 0) && fine(p.w, p.n > 1 ? p.w_stride : 0) &&
          (p.num_experts == 1 || p.w_matrix % 16 == 0) && p.a_scales_stride < (1 << 20) && p.k < (1 << 30) &&
-         p.rows < (1 << 30);
+         p.rows < (1 << 30) && p.out_stride < (1 << 22);
 }
 
 template <int FW, int FA, typename O>
