@@ -195,11 +195,10 @@ __device__ __forceinline__ void store_packed8(bf16_t* p, int left, const u32x4& 
 // ---------------------------------------------------------------------------
 constexpr int kTile = 256, kStage = 2 * kTile * 128 + kTile * 4 + 256;
 
-// A tile's operands as buffers that end with its last row: matrix and rows, the rows' scales, and the
-// columns' (those of two blocks, or of one and wb = 0).
+// A tile's operands as buffers that end with its last row, and where its rows' and columns' scales begin.
 struct Operands {
-  u32x4 w, a, as, ws;
-  int wb;
+  u32x4 w, a;
+  uint32_t as, ws;
 };
 
 __device__ __forceinline__ u32x4 lds_read16(uint32_t at) {
@@ -208,6 +207,15 @@ __device__ __forceinline__ u32x4 lds_read16(uint32_t at) {
 __device__ __forceinline__ float lds_read4(uint32_t at) {
   return *reinterpret_cast<const __attribute__((address_space(3))) float*>((uintptr_t)at);
 }
+// The kernel's first argument read anew where it is used, once a tile: held over the loop, its fields
+// would take the scalar registers that the loop needs.
+typedef const __attribute__((address_space(4))) muon_product_args* ArgsPtr;
+__device__ __forceinline__ ArgsPtr args_again() {
+  ArgsPtr a = (ArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(a));
+  return a;
+}
+
 template <int FW, int FA>
 __global__ void __launch_bounds__(512, 2)
 ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
@@ -230,21 +238,22 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
   if (index >= end || !find_tile(runs, E, rows, kTile, tiles_n, index, tile)) return;
 
   const uint32_t w_pitch = (uint32_t)p.w_stride, a_pitch = (uint32_t)p.a_stride, s_pitch = (uint32_t)p.a_scales_stride * 4u;
+  const u32x4 as_all = buffer_of(p.a_scales, (rows - 1) * s_pitch + KB * 4), ws_all = buffer_of(p.w_scales, E * NB * KB * 4);
   auto operands = [&](const ExpertTile& x) {
+    const ArgsPtr p = args_again();
     const int64_t n0 = (int64_t)x.tn * kTile;
-    const int wl = (int)min((int64_t)kTile, p.n - n0) - 1, al = x.rows - 1, wb = 2 * x.tn + 1 < NB ? 1 : 0;
-    return Operands{buffer_of(static_cast<const uint8_t*>(p.w) + (int64_t)x.e * p.w_matrix + n0 * p.w_stride, wl * w_pitch + K),
-                    buffer_of(static_cast<const uint8_t*>(p.a) + (int64_t)x.row0 * p.a_stride, al * a_pitch + K),
-                    buffer_of(p.a_scales + (int64_t)x.row0 * p.a_scales_stride, al * s_pitch + KB * 4),
-                    buffer_of(p.w_scales + ((int64_t)x.e * NB + 2 * x.tn) * KB, (wb + 1) * KB * 4), wb};
+    const int wl = (int)min((int64_t)kTile, p->n - n0) - 1, al = x.rows - 1;
+    return Operands{buffer_of(static_cast<const uint8_t*>(p->w) + (int64_t)x.e * p->w_matrix + n0 * p->w_stride, wl * w_pitch + K),
+                    buffer_of(static_cast<const uint8_t*>(p->a) + (int64_t)x.row0 * p->a_stride, al * a_pitch + K),
+                    (uint32_t)x.row0 * s_pitch, (uint32_t)(x.e * NB + 2 * x.tn) * KB * 4};
   };
   // Block kb of a tile to a stage, load `part` of nine: this wave's 32 rows of each operand, eight a
   // load, 16-byte piece c of row r in slot slot_of(r, c), then scales.  Pieces past the end of a row are
   // cleared by settle().
-  auto piece = [&](int j) { return ((lane & 7) ^ ((4 * j + (lane >> 4)) & 7)) * 16; };
+  auto piece_of = [](int l, int j) { return ((l & 7) ^ ((4 * j + (l >> 4)) & 7)) * 16; };
   const uint32_t row = 32 * w + (lane >> 3);
-  const uint32_t w_off[2] = {row * w_pitch + piece(0), row * w_pitch + piece(1)};
-  const uint32_t a_off[2] = {row * a_pitch + piece(0), row * a_pitch + piece(1)};
+  const uint32_t w_off[2] = {row * w_pitch + piece_of(lane, 0), row * w_pitch + piece_of(lane, 1)};
+  const uint32_t a_off[2] = {row * a_pitch + piece_of(lane, 0), row * a_pitch + piece_of(lane, 1)};
   const uint32_t s_off = w < 4 ? (64 * w + lane) * s_pitch : (lane & 1) * KB * 4;
   auto issue = [&](const Operands& o, int kb, uint32_t stage, int part) {
     if (part < 8) {
@@ -253,9 +262,9 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
       if (part & 1) lds_dma16(o.a, a_off[j & 1], kb * 128 + 8 * j * a_pitch, to + kTile * 128);
       else lds_dma16(o.w, w_off[j & 1], kb * 128 + 8 * j * w_pitch, to);
     } else if (w < 4) {
-      lds_dma4(o.as, s_off, kb * 4, stage + 2 * kTile * 128 + w * 256);
+      lds_dma4(as_all, s_off, o.as + kb * 4, stage + 2 * kTile * 128 + w * 256);
     } else if (w == 4) {
-      lds_dma4(o.ws, o.wb ? s_off : 0u, kb * 4, stage + 2 * kTile * 128 + kTile * 4);
+      lds_dma4(ws_all, s_off, o.ws + kb * 4, stage + 2 * kTile * 128 + kTile * 4);
     }
   };
   // this wave's loads have arrived, block kb's in the given stage
@@ -265,10 +274,12 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
     else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     stores = false;
     if (kb * 128 + 128 > K) {
+      int l = lane;   // formed here: registers are short in the loop
+      asm volatile("" : "+v"(l));
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (kb * 128 + piece(j) >= K) {
-          u32x4* to = reinterpret_cast<u32x4*>(lds + (stage - lds0) + w * 4096 + lane * 16 + j * 1024);
+        if (kb * 128 + piece_of(l, j) >= K) {
+          u32x4* to = reinterpret_cast<u32x4*>(lds + (stage - lds0) + w * 4096 + l * 16 + j * 1024);
           to[0] = u32x4{};
           to[kTile * 8] = u32x4{};
         }
@@ -294,20 +305,39 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
   const uint32_t sat = 2 * kTile * 128 + (wm * 64 + q) * 4, swat = 2 * kTile * 128 + kTile * 4 + wn * 4;
   i32x8 fw[2][2], fa[4];
   float sn[4], swn;
+  auto first_fragments = [&](uint32_t stage) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    fa[j] = read(here + alo + j * 2048, here + ahi + j * 2048);
-    sn[j] = lds_read4(here + sat + j * 64);
-  }
+    for (int j = 0; j < 4; ++j) {
+      fa[j] = read(stage + alo + j * 2048, stage + ahi + j * 2048);
+      sn[j] = lds_read4(stage + sat + j * 64);
+    }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) fw[0][i] = read(here + wlo + i * 2048, here + whi + i * 2048);
-  swn = lds_read4(here + swat);
+    for (int i = 0; i < 2; ++i) fw[0][i] = read(stage + wlo + i * 2048, stage + whi + i * 2048);
+    swn = lds_read4(stage + swat);
+  };
+  first_fragments(here);
 
   for (bool more = true; more;) {
     ExpertTile next = tile;   // the last tile loads its own first blocks once more
     index += step;
     more = index < end && find_tile(runs, E, rows, kTile, tiles_n, index, next);
     const Operands then = operands(next);
+    if (wm * 64 >= tile.rows) {   // on a short last tile one wave of each SIMD only loads
+      for (int kb = 0; kb < KB; ++kb) {
+        settle(kb + 1 < KB ? kb + 1 : 0, there);
+        lds_barrier();
+        const bool ahead = kb + 2 < KB;
+#pragma unroll
+        for (int x = 0; x < 9; ++x) issue(ahead ? cur : then, ahead ? kb + 2 : kb + 2 - KB, here, x);
+        const uint32_t x = here;
+        here = there;
+        there = x;
+      }
+      first_fragments(here);
+      tile = next;
+      cur = then;
+      continue;
+    }
     f32x4 acc[8][4] = {};
     for (int kb = 0; kb < KB; ++kb) {
       const bool ahead = kb + 2 < KB;
@@ -353,8 +383,10 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
       there = x;
     }
     const int64_t n0 = (int64_t)tile.tn * kTile + wn * 128;
-    bf16_t* out = static_cast<bf16_t*>(p.out) + (int64_t)(tile.row0 + wm * 64) * p.out_stride + n0;
-    const int n_left = (int)min((int64_t)128, p.n - n0), r_left = tile.rows - wm * 64;
+    const ArgsPtr again = args_again();
+    bf16_t* out = static_cast<bf16_t*>(again->out) + (int64_t)(tile.row0 + wm * 64) * again->out_stride + n0;
+    const uint32_t out_pitch = (uint32_t)again->out_stride;
+    const int n_left = (int)min((int64_t)128, again->n - n0), r_left = tile.rows - wm * 64;
     int lq = lane;   // formed here: registers are short in the loop
     asm volatile("" : "+v"(lq));
     const int c0 = ((lq >> 4) & 1) * 16 + (lq >> 5) * 8;
@@ -369,7 +401,7 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
         const auto y = __builtin_amdgcn_permlane16_swap(pack_bf16(acc[i][j][2], acc[i][j][3]),
                                                         pack_bf16(acc[i + 1][j][2], acc[i + 1][j][3]), false, false);
         const int r = j * 16 + lq, n = i * 16 + c0;
-        if (r < r_left) store_packed8(out + (__umul24(r, (uint32_t)p.out_stride) + n), n_left - n, u32x4{x[0], y[0], x[1], y[1]});
+        if (r < r_left) store_packed8(out + (__umul24(r, out_pitch) + n), n_left - n, u32x4{x[0], y[0], x[1], y[1]});
       }
     }
     // sixteen stores, and nothing else, behind the loads that settle() waits for next
@@ -388,7 +420,8 @@ bool whole_pieces(const muon_product_args& p) {
   };
   return p.k % 16 == 0 && fine(p.a, p.rows > 1 ? p.a_stride : 0) && fine(p.w, p.n > 1 ? p.w_stride : 0) &&
          (p.num_experts == 1 || p.w_matrix % 16 == 0) && p.a_scales_stride < (1 << 20) && p.k < (1 << 30) &&
-         p.rows < (1 << 30) && p.out_stride < (1 << 22);
+         p.rows < (1 << 30) && p.out_stride < (1 << 22) && p.rows * (p.rows > 1 ? p.a_scales_stride : 1) < (1 << 30) &&
+         p.num_experts * ((p.n + 127) / 128) * ((p.k + 127) / 128) < (1 << 30);
 }
 
 template <int FW, int FA, typename O>
