@@ -106,21 +106,20 @@ ex_weight_grad(muon_weight_grad_args p, Dest d, int64_t tn, int64_t tk) {
 // whole 16-byte pieces.
 //
 // 64 rows of both operands at a time come straight from global memory into one
-// of two stages; a wave multiplies a stage in two halves of 32 rows, 16
-// instructions of 32 cycles each.  The waves form two groups, one wave of each
-// on a SIMD, the second a quarter step behind, so that one reads its fragments
-// (transposed, 48 registers) while the other multiplies; a barrier ends each
-// quarter.  A stage is loaded while the other is worked on: each wave issues its
-// share before its first reads and waits for it as late as the other group's
-// order allows.  x's columns are the instruction's rows, so that a lane ends with
-// runs of four along k, eight after one exchange with the lane 32 away.
+// of two stages; a wave multiplies a stage in four steps of 16 rows, eight
+// instructions of 32 cycles each, and reads the next step's fragments
+// (transposed) between them.  The one barrier of a stage stands before its last
+// step: then every wave has read the stage, so that the one after the next may
+// be loaded into it, and every wave's loads of the next stage, a whole stage old,
+// are there, so that the last step reads the first fragments of the next stage.
+// Stages follow one another over the tiles without a gap.  x's columns are the
+// instruction's rows, so that a lane ends with runs of four along k, eight after
+// one exchange with the lane 32 away.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 256, kRows = 64, kStage = 2 * kRows * kTile * 2;
 
-// A tile's operands at its first columns, its run of rows and its place in the output.
+// A tile: its columns, its run of rows and its place in the output.
 struct Tile {
-  const bf16_t* dy;
-  const bf16_t* x;
   int lo, hi;
   int e, part, n0, k0;
 };
@@ -161,10 +160,12 @@ template <typename O>
 __global__ void __launch_bounds__(512, 2)
 ex_weight_grad_tiled(muon_weight_grad_args p, Dest d, uint32_t tn, uint32_t tk) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
+  __shared__ int32_t runs[MUON_ROUTE_MAX_EXPERTS + 1];
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6), wk = w & 1, wn = (w >> 1) & 3;
-  const bool second = w >= 4;
-  const int rows = (int)p.rows;
+  const int rows = (int)p.rows, E = (int)p.num_experts;
+  for (int e = t; e <= E; e += 512) runs[e] = p.offsets ? p.offsets[e] : e ? rows : 0;
+  __syncthreads();
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
 
   // An expert's tiles, which share their operands, are dealt in eight runs to the XCDs (every eighth
@@ -173,7 +174,7 @@ ex_weight_grad_tiled(muon_weight_grad_args p, Dest d, uint32_t tn, uint32_t tk) 
   const bool deal = each >= 64;
   const uint32_t from = deal ? (uint32_t)((uint64_t)each * xcd / 8) : 0;
   const uint32_t mine = deal ? (uint32_t)((uint64_t)each * (xcd + 1) / 8) - from : each;
-  const uint32_t total = mine * (uint32_t)p.num_experts, step = deal ? gridDim.x >> 3 : gridDim.x;
+  const uint32_t total = mine * (uint32_t)E, step = deal ? gridDim.x >> 3 : gridDim.x;
   uint32_t index = deal ? blockIdx.x >> 3 : blockIdx.x;
   if (index >= total) return;
   auto tile_at = [&](uint32_t i) {
@@ -184,40 +185,62 @@ ex_weight_grad_tiled(muon_weight_grad_args p, Dest d, uint32_t tn, uint32_t tk) 
     x.n0 = (int)__builtin_amdgcn_readfirstlane(u / tk) * kTile;
     x.k0 = (int)__builtin_amdgcn_readfirstlane(u % tk) * kTile;
     int lo, hi;
-    run_of(p.offsets, x.e, rows, lo, hi);
+    run_of(runs, x.e, rows, lo, hi);
     part_of(x.part, d.parts, kRows, lo, hi);
     x.lo = __builtin_amdgcn_readfirstlane(lo);
     x.hi = __builtin_amdgcn_readfirstlane(hi);
-    x.dy = static_cast<const bf16_t*>(p.dy) + x.n0;
-    x.x = static_cast<const bf16_t*>(p.x) + x.k0;
     return x;
   };
 
   // Rows first .. first + 63 to a stage: this wave's eight rows of each operand, two a load, 16-byte
   // piece c of row r in slot c ^ 4 (r % 4), so that the four rows of a transposing read lie on different
-  // banks.  Rows past the run's end take some row and are cleared by settle(), columns past the matrix
-  // its tile's first ones.
-  const int piece[2] = {(lane & 31) ^ (4 * (lane >> 5)), (lane & 31) ^ (4 * (lane >> 5) + 8)};   // of rows 2 j + (lane >> 5), j even / odd
-  auto issue = [&](const Tile& x, int first, uint32_t stage) {
-    const int base = min(first, rows - 1);
-    const bf16_t* dy = x.dy + (int64_t)base * p.dy_stride;
-    const bf16_t* xx = x.x + (int64_t)base * p.x_stride;
-    const uint32_t to = stage + w * 4096;
-    int r0 = 8 * w + (lane >> 5);
-    asm volatile("" : "+v"(r0));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t r = min(r0 + 2 * j, rows - 1 - base), c = piece[j & 1] * 8;
-      lds_dma16(dy, (__umul24(r, (uint32_t)p.dy_stride) + (x.n0 + c < p.n ? c : 0u)) * 2, to + j * 1024);
-      lds_dma16(xx, (__umul24(r, (uint32_t)p.x_stride) + (x.k0 + c < p.k ? c : 0u)) * 2, to + kStage / 2 + j * 1024);
-    }
+  // banks.  The buffers end with the run; rows past it are cleared by settle().
+  const uint32_t d_pitch = (uint32_t)p.dy_stride * 2, x_pitch = (uint32_t)p.x_stride * 2;
+  auto lane_off = [&](uint32_t pitch, int j) {   // rows 2 j + (lane >> 5), j even / odd
+    return (lane >> 5) * pitch + (uint32_t)((lane & 31) ^ (4 * (lane >> 5) + 8 * j)) * 16;
   };
-  auto settle = [&](int first, int hi, uint32_t stage) {
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-    if (first + kRows > hi) {
+  const uint32_t d_off[2] = {lane_off(d_pitch, 0), lane_off(d_pitch, 1)}, x_off[2] = {lane_off(x_pitch, 0), lane_off(x_pitch, 1)};
+  Tile load = tile_at(index);       // the tile being loaded, its next rows, whether there are any
+  uint32_t load_index = index;
+  int first = load.lo;
+  bool live = true;
+  struct Rows64 {
+    u32x4 dy, x;
+    int first, hi;
+  };
+  auto next_rows = [&]() {
+    if (!live) return Rows64{buffer_of(p.dy, 0), buffer_of(p.x, 0), 0, 0};
+    const int left = load.hi - first, n = left < kRows ? left : kRows;
+    const Rows64 r{buffer_of(static_cast<const bf16_t*>(p.dy) + (int64_t)first * p.dy_stride + load.n0,
+                             n > 0 ? (n - 1) * d_pitch + (uint32_t)(p.n - load.n0) * 2 : 0),
+                   buffer_of(static_cast<const bf16_t*>(p.x) + (int64_t)first * p.x_stride + load.k0,
+                             n > 0 ? (n - 1) * x_pitch + (uint32_t)(p.k - load.k0) * 2 : 0),
+                   first, load.hi};
+    first += kRows;
+    if (first >= load.hi) {
+      load_index += step;
+      live = load_index < total;
+      if (live) load = tile_at(load_index);
+      first = load.lo;
+    }
+    return r;
+  };
+  auto issue = [&](const Rows64& r, uint32_t stage, int part) {   // load `part` of eight
+    const int j = part >> 1;
+    const uint32_t to = stage + w * 4096 + j * 1024;
+    if (part & 1) lds_dma16(r.x, x_off[j & 1], (8 * w + 2 * j) * x_pitch, to + kStage / 2);
+    else lds_dma16(r.dy, d_off[j & 1], (8 * w + 2 * j) * d_pitch, to);
+  };
+  constexpr int kStores = sizeof(O) == 2 ? 16 : 32;
+  bool stores = false;   // a tile's stores, and nothing else, are behind the loads that settle() waits for
+  auto settle = [&](int f, int hi, uint32_t stage) {
+    if (stores) __builtin_amdgcn_s_waitcnt(vmcnt_imm(kStores));   // counted in the order of issue
+    else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    stores = false;
+    if (f + kRows > hi) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (first + 8 * w + 2 * j + (lane >> 5) >= hi) {
+        if (f + 8 * w + 2 * j + (lane >> 5) >= hi) {
           u32x4* to = reinterpret_cast<u32x4*>(lds + (stage - lds0) + w * 4096 + lane * 16 + j * 1024);
           to[0] = u32x4{};
           to[kStage / 32] = u32x4{};
@@ -225,12 +248,20 @@ ex_weight_grad_tiled(muon_weight_grad_args p, Dest d, uint32_t tn, uint32_t tk) 
     }
   };
 
-  Tile cur = tile_at(index);
   uint32_t here = lds0, there = lds0 + kStage;
-  issue(cur, cur.lo, here);
-  settle(cur.lo, cur.hi, here);
+  int f1, h1;   // rows of the stage after the one being worked on
+  {
+    const Rows64 r0 = next_rows();
+#pragma unroll
+    for (int x = 0; x < 8; ++x) issue(r0, here, x);
+    const Rows64 r1 = next_rows();
+#pragma unroll
+    for (int x = 0; x < 8; ++x) issue(r1, there, x);
+    f1 = r1.first;
+    h1 = r1.hi;
+    settle(r0.first, r0.hi, here);
+  }
   lds_barrier();
-  if (second) lds_barrier();
   // Of 32 columns (block b of the operand's eight) a lane reads rows 8 (G / 2) + s / 4 and four below, columns
   // 16 (G % 2) + 4 (s % 4) on, in 16-lane group G at lane s.
   const int G = lane >> 4, s4 = lane & 15;
@@ -242,60 +273,53 @@ ex_weight_grad_tiled(muon_weight_grad_args p, Dest d, uint32_t tn, uint32_t tk) 
   for (int i = 0; i < 4; ++i) xa[i] = column(4 * wk + i) + kStage / 2;
 #pragma unroll
   for (int j = 0; j < 2; ++j) da[j] = column(2 * wn + j);
+  bf16x8 fx[2][4], fd[2][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) fx[0][i] = read_tr(here + xa[i]);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) fd[0][j] = read_tr(here + da[j]);
 
-  for (bool more = true; more;) {
-    index += step;
-    more = index < total;
-    const Tile next = more ? tile_at(index) : cur;   // the last tile loads its own first rows once more
+  for (; index < total; index += step) {
+    const Tile cur = tile_at(index);
     f32x16 acc[4][2] = {};
-    for (int first = cur.lo, last = 0; !last; first += kRows) {
-      last = first + kRows >= cur.hi;
-      const Tile& of = last ? next : cur;
-      const int nf = last ? next.lo : first + kRows, nh = last ? next.hi : cur.hi;
-      issue(of, nf, there);
+    for (int at = cur.lo, last = 0; !last; at += kRows) {
+      last = at + kRows >= cur.hi;
+      const Rows64 r = next_rows();
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        bf16x8 fx[2][4], fd[2][2];
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) fx[kk][i] = read_tr(here + xa[i] + (2 * half + kk) * 16 * 512);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) fd[kk][j] = read_tr(here + da[j] + (2 * half + kk) * 16 * 512);
+      for (int kk = 0; kk < 4; ++kk) {
+        if (kk == 3) {   // the stage is read, the next one is there
+          settle(f1, h1, there);
+          lds_barrier();
         }
-        if (half == 1 && second) settle(nf, nh, there);
-        lds_barrier();
-        __builtin_amdgcn_s_setprio(1);
+        const uint32_t of = kk < 3 ? here + (kk + 1) * 16 * 512 : there;
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fx[kk][i], fd[kk][j], acc[i][j], 0, 0, 0);
-              __builtin_amdgcn_sched_barrier(0);
-            }
-        __builtin_amdgcn_s_setprio(0);
-        if (half == 1 && !second) settle(nf, nh, there);
-        if (half == 1 && last) {
-          O* out = static_cast<O*>(d.base) + cur.part * d.part + cur.e * d.matrix;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int64_t n = cur.n0 + wn * 64 + j * 32 + (lane & 31);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              store_block<O>(out + n * d.stride, cur.k0 + wk * 128 + i * 32, p.k, acc[i][j], lane >> 5, n < p.n);
-          }
+        for (int x = 0; x < 8; ++x) {
+          acc[x >> 1][x & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fx[kk & 1][x >> 1], fd[kk & 1][x & 1], acc[x >> 1][x & 1], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+          if (x < 4) fx[~kk & 1][x] = read_tr(of + xa[x]);
+          else if (x < 6) fd[~kk & 1][x - 4] = read_tr(of + da[x - 4]);
+          if (kk == 3) issue(r, here, x);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        lds_barrier();
       }
+      f1 = r.first;
+      h1 = r.hi;
       const uint32_t x = here;
       here = there;
       there = x;
     }
-    cur = next;
+    O* out = static_cast<O*>(d.base) + cur.part * d.part + cur.e * d.matrix;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t n = cur.n0 + wn * 64 + j * 32 + (lane & 31);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        store_block<O>(out + n * d.stride, cur.k0 + wk * 128 + i * 32, p.k, acc[i][j], lane >> 5, n < p.n);
+    }
+    stores = cur.n0 + wn * 64 + 64 <= p.n && cur.k0 + wk * 128 + 128 <= p.k;
   }
-  if (!second) lds_barrier();
+  // the loads that are still on their way go to this workgroup's memory
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
 }
 
 // dw = the sum of the parts, in their order.
