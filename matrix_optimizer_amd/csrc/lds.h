@@ -92,4 +92,23 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// Registers a and b against lane bit 3 (4): afterwards a holds what lanes with the bit clear had in both, in
+// the lanes that had it and in their partners, and b what the others had.
+__device__ __forceinline__ void swap_lanes8(u32x4& a, u32x4& b) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int x = (int)a[i], y = (int)b[i];
+    a[i] = (uint32_t)__builtin_amdgcn_update_dpp(x, y, 0x128, 0xf, 0xc, false);   // lanes 8-15 of 16 from 8 below
+    b[i] = (uint32_t)__builtin_amdgcn_update_dpp(y, x, 0x128, 0xf, 0x3, false);
+  }
+}
+__device__ __forceinline__ void swap_lanes16(u32x4& a, u32x4& b) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const auto v = __builtin_amdgcn_permlane16_swap(a[i], b[i], false, false);
+    a[i] = v[0];
+    b[i] = v[1];
+  }
+}
+
 }  // namespace muon

@@ -168,10 +168,11 @@ ex_product(muon_product_args p, uint32_t tiles_n) {
   }
 }
 
-// Eight columns of a bf16 row, of which `left` belong to it.
+// Eight columns of a bf16 row, of which `left` belong to it.  Stored past the cache, where the operands of the
+// tiles to come are.
 __device__ __forceinline__ void store_packed8(bf16_t* p, int left, const u32x4& v) {
   if (left >= 8) {
-    *reinterpret_cast<u32x4_any*>(p) = v;
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(p));
   } else {
 #pragma unroll
     for (int r = 0; r < 7; ++r)
@@ -389,19 +390,28 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
     const int n_left = (int)min((int64_t)128, again->n - n0), r_left = tile.rows - wm * 64;
     int lq = lane;   // formed here: registers are short in the loop
     asm volatile("" : "+v"(lq));
-    const int c0 = ((lq >> 4) & 1) * 16 + (lq >> 5) * 8;
-    lq &= 15;
+    const int c0 = ((lq >> 3) & 1) * 32 + ((lq >> 4) & 1) * 16 + (lq >> 5) * 8;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        // lane groups 0 and 2 take the fragment's other four columns from 1 and 3, which take theirs of the next
-        const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16(acc[i][j][0], acc[i][j][1]),
-                                                        pack_bf16(acc[i + 1][j][0], acc[i + 1][j][1]), false, false);
-        const auto y = __builtin_amdgcn_permlane16_swap(pack_bf16(acc[i][j][2], acc[i][j][3]),
-                                                        pack_bf16(acc[i + 1][j][2], acc[i + 1][j][3]), false, false);
-        const int r = j * 16 + lq, n = i * 16 + c0;
-        if (r < r_left) store_packed8(out + (__umul24(r, out_pitch) + n), n_left - n, u32x4{x[0], y[0], x[1], y[1]});
+      for (int i = 0; i < 8; i += 4) {
+        u32x4 v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // lane groups 0 and 2 take the fragment's other four columns from 1 and 3, which take theirs of the next
+          const f32x4 &a = acc[i + 2 * h][j], &b = acc[i + 2 * h + 1][j];
+          const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16(a[0], a[1]), pack_bf16(b[0], b[1]), false, false);
+          const auto y = __builtin_amdgcn_permlane16_swap(pack_bf16(a[2], a[3]), pack_bf16(b[2], b[3]), false, false);
+          v[h] = u32x4{x[0], y[0], x[1], y[1]};
+        }
+        // lanes 8-15 of 16 take the second 32 columns of the rows of lanes 0-7, which leave them theirs: 128
+        // bytes of a row side by side
+        swap_lanes8(v[0], v[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = j * 16 + 8 * h + (lq & 7), n = i * 16 + c0;
+          if (r < r_left) store_packed8(out + (__umul24(r, out_pitch) + n), n_left - n, v[h]);
+        }
       }
     }
     // sixteen stores, and nothing else, behind the loads that settle() waits for next

@@ -129,30 +129,54 @@ __device__ __forceinline__ bf16x8 read_tr(uint32_t at) {
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-template <typename O>
-__device__ __forceinline__ void store_block(O* row, int64_t k0, int64_t K, const f32x16& v, int half, bool live);
-// Columns k0 .. k0+31 of a row, of which lanes below 32 hold runs of four at 8 q and the others at 8 q + 4.
-template <>
-__device__ __forceinline__ void store_block<float>(float* row, int64_t k0, int64_t K, const f32x16& v, int half, bool live) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int64_t k = k0 + 8 * q + 4 * half;
-    if (live && k < K)   // K is a multiple of 8
-      *reinterpret_cast<u32x4_any*>(row + k) = u32x4{__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-                                                     __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])};
-  }
+// Four 16-byte pieces a lane of 32 rows of eight pieces, those of lanes n and n + 32 alternately the pieces
+// of row n, dealt anew so that each register holds eight whole rows, 128 bytes in a row at a time: row
+// 8 s + lane % 8, piece 2 (lane / 8 % 4) + lane / 32.  Stored past the cache, where the operands of the
+// tiles to come are: 64 [7168, 2048] from one stage each in 333 us, 467 through the cache, 499 by 32 bytes a
+// row as the pieces come.
+__device__ __forceinline__ void whole_rows(u32x4 (&r)[4]) {
+  swap_lanes8(r[0], r[1]);
+  swap_lanes8(r[2], r[3]);
+  swap_lanes16(r[0], r[2]);
+  swap_lanes16(r[1], r[3]);
 }
-template <>
-__device__ __forceinline__ void store_block<bf16_t>(bf16_t* row, int64_t k0, int64_t K, const f32x16& v, int half, bool live) {
+
+// 32 rows of 64 (bf16) or 32 (fp32) columns from an accumulator pair or one accumulator; `k_left` columns and
+// `n_left` rows belong to the matrix.
+__device__ __forceinline__ void store_rows(bf16_t* out, int64_t stride, int k_left, int n_left, const f32x16& v0, const f32x16& v1) {
+  const int lane = threadIdx.x & 63;
+  u32x4 r[4];
 #pragma unroll
-  for (int q = 0; q < 4; q += 2) {
+  for (int s = 0; s < 4; ++s) {
+    const f32x16& v = s < 2 ? v0 : v1;
+    const int q = 2 * (s & 1);
     // lanes below 32 keep run q and take its other half, the others run q + 1
     const auto a = __builtin_amdgcn_permlane32_swap(pack_bf16(v[4 * q], v[4 * q + 1]), pack_bf16(v[4 * q + 4], v[4 * q + 5]),
                                                     false, false);
     const auto b = __builtin_amdgcn_permlane32_swap(pack_bf16(v[4 * q + 2], v[4 * q + 3]),
                                                     pack_bf16(v[4 * q + 6], v[4 * q + 7]), false, false);
-    const int64_t k = k0 + 8 * (q + half);
-    if (live && k < K) *reinterpret_cast<u32x4_any*>(row + k) = u32x4{a[0], b[0], a[1], b[1]};
+    r[s] = u32x4{a[0], b[0], a[1], b[1]};
+  }
+  whole_rows(r);
+  const int k = 8 * (2 * ((lane >> 3) & 3) + (lane >> 5));
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int n = 8 * s + (lane & 7);
+    if (k < k_left && n < n_left) __builtin_nontemporal_store(r[s], reinterpret_cast<u32x4_any*>(out + n * stride + k));   // columns are whole pieces
+  }
+}
+__device__ __forceinline__ void store_rows(float* out, int64_t stride, int k_left, int n_left, const f32x16& v) {
+  const int lane = threadIdx.x & 63;
+  u32x4 r[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    r[s] = u32x4{__float_as_uint(v[4 * s]), __float_as_uint(v[4 * s + 1]), __float_as_uint(v[4 * s + 2]), __float_as_uint(v[4 * s + 3])};
+  whole_rows(r);
+  const int k = 4 * (2 * ((lane >> 3) & 3) + (lane >> 5));
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int n = 8 * s + (lane & 7);
+    if (k < k_left && n < n_left) __builtin_nontemporal_store(r[s], reinterpret_cast<u32x4_any*>(out + n * stride + k));
   }
 }
 
@@ -308,15 +332,18 @@ ex_weight_grad_tiled(muon_weight_grad_args p, Dest d, uint32_t tn, uint32_t tk) 
       here = there;
       there = x;
     }
-    O* out = static_cast<O*>(d.base) + cur.part * d.part + cur.e * d.matrix;
+    const int n0 = cur.n0 + wn * 64, k0 = cur.k0 + wk * 128;
+    O* out = static_cast<O*>(d.base) + cur.part * d.part + cur.e * d.matrix + n0 * d.stride + k0;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t n = cur.n0 + wn * 64 + j * 32 + (lane & 31);
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        store_block<O>(out + n * d.stride, cur.k0 + wk * 128 + i * 32, p.k, acc[i][j], lane >> 5, n < p.n);
-    }
-    stores = cur.n0 + wn * 64 + 64 <= p.n && cur.k0 + wk * 128 + 128 <= p.k;
+      for (int i = 0; i < 4; ++i) {
+        O* at = out + 32 * j * d.stride + 32 * i;
+        const int k_left = (int)p.k - k0 - 32 * i, n_left = (int)p.n - n0 - 32 * j;
+        if constexpr (sizeof(O) == 4) store_rows(at, d.stride, k_left, n_left, acc[i][j]);
+        else if (i % 2 == 0) store_rows(at, d.stride, k_left, n_left, acc[i][j], acc[i + 1][j]);
+      }
+    stores = n0 + 64 <= p.n && k0 + 128 <= p.k;
   }
   // the loads that are still on their way go to this workgroup's memory
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
