@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(256)
 ex_product(muon_product_args p, uint32_t tiles_n) {
   typedef Block<FW, FA, O> Blk;
   constexpr int BM = 128, BN = 128;
-  __shared__ u32x4 lds[(BM + BN) * 8];
+  __shared__ u32x4 lds[2][(BM + BN) * 8];
   const int t = threadIdx.x, lane = t & 63, g = lane >> 4, q = lane & 15, w = t >> 6, wn = w & 1, wm = w >> 1;
   const int64_t KB = (p.k + 127) / 128, NB = (p.n + 127) / 128;
   ExpertTile tile;
@@ -116,6 +116,7 @@ ex_product(muon_product_args p, uint32_t tiles_n) {
     const uint8_t* W = static_cast<const uint8_t*>(p.w) + (int64_t)tile.e * p.w_matrix + n0 * p.w_stride;
     const uint8_t* A = static_cast<const uint8_t*>(p.a) + (int64_t)tile.row0 * p.a_stride;
     const float* ws = p.w_scales + ((int64_t)tile.e * NB + tile.tn) * KB;
+    __syncthreads();   // the tile before has been multiplied
     const float* as[4];
     bool live[4];
 #pragma unroll
@@ -125,27 +126,37 @@ ex_product(muon_product_args p, uint32_t tiles_n) {
       as[j] = p.a_scales + (int64_t)(tile.row0 + (live[j] ? r : 0)) * p.a_scales_stride;
     }
     f32x4 acc[4][4] = {};
-    for (int64_t b = 0; b < KB; ++b) {
-      __syncthreads();
+    u32x4 v[8];
+    auto load = [&](int64_t b) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = (t >> 3) + 32 * i, c = t & 7;   // rows 0 .. 127 of W, then of A
-        u32x4 v = {};
+        v[i] = u32x4{};
         if (i < 4) {
-          if (n0 + r < p.n) v = load16(W + r * p.w_stride, b * 128 + c * 16, p.k);
+          if (n0 + r < p.n) v[i] = load16(W + r * p.w_stride, b * 128 + c * 16, p.k);
         } else {
-          if (r - BN < tile.rows) v = load16(A + (int64_t)(r - BN) * p.a_stride, b * 128 + c * 16, p.k);
+          if (r - BN < tile.rows) v[i] = load16(A + (int64_t)(r - BN) * p.a_stride, b * 128 + c * 16, p.k);
         }
-        lds[r * 8 + slot_of(r, c)] = v;
+      }
+    };
+    load(0);
+    for (int64_t b = 0; b < KB; ++b) {
+      // block b is written while others still multiply the one before from the other stage
+      u32x4* stage = lds[b & 1];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = (t >> 3) + 32 * i, c = t & 7;
+        stage[r * 8 + slot_of(r, c)] = v[i];
       }
       __syncthreads();
+      if (b + 1 < KB) load(b + 1);
       const float sw = ws[b];
       typename Blk::Frag fw[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) fw[i] = Blk::template make<FW>(fragment(lds, wn * 64 + i * 16 + q, g));
+      for (int i = 0; i < 4; ++i) fw[i] = Blk::template make<FW>(fragment(stage, wn * 64 + i * 16 + q, g));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const typename Blk::Frag fa = Blk::template make<FA>(fragment(lds, BN + wm * 64 + j * 16 + q, g));
+        const typename Blk::Frag fa = Blk::template make<FA>(fragment(stage, BN + wm * 64 + j * 16 + q, g));
         const float s = live[j] ? as[j][b] * sw : 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -423,6 +434,135 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
 }
 
+// ---------------------------------------------------------------------------
+// Few rows an expert: the matrices' bytes are what counts, and each is used by
+// one wave only, so that they go from memory to registers.
+//
+// A wave takes 16 columns (matrix rows) against up to 64 rows, 16 at a time, and
+// KS waves of a workgroup share the blocks of k in groups of U; their sums are
+// added in the order of the waves.  Any size, stride and alignment.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ i32x8 join(const u32x4& x, const u32x4& y) {
+  return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
+}
+
+// U blocks from block b on: FULL: they all lie within the row.
+template <int FW, int FA, typename O, int NT, int U, bool FULL>
+__device__ __forceinline__ void few_blocks(const uint8_t* w, const uint8_t* const (&a)[NT], const float* ws,
+                                           const float* const (&as)[NT], int64_t b, int64_t KB, int64_t K, f32x4 (&acc)[NT]) {
+  typedef Block<FW, FA, O> Blk;
+  const int g = (threadIdx.x & 63) >> 4;
+  u32x4 wv[U][2], av[U][NT][2];
+  float sw[U], sa[U][NT];
+  auto get = [&](const uint8_t* row, int64_t k) {
+    return FULL ? (u32x4)*reinterpret_cast<const u32x4_any*>(row + k) : load16(row, k, K);
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t k = (b + u) * 128 + g * 16;
+    wv[u][0] = get(w, k);
+    wv[u][1] = get(w, k + 64);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t k = (b + u) * 128 + g * 16;
+    const bool in = FULL || b + u < KB;
+    sw[u] = in ? ws[b + u] : 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      av[u][t][0] = get(a[t], k);
+      av[u][t][1] = get(a[t], k + 64);
+      sa[u][t] = in ? as[t][b + u] : 0.f;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const typename Blk::Frag fw = Blk::template make<FW>(join(wv[u][0], wv[u][1]));
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const typename Blk::Frag fa = Blk::template make<FA>(join(av[u][t][0], av[u][t][1]));
+      const f32x4 d = Blk::mfma(fw, fa);
+      const float s = sa[u][t] * sw[u];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[t][r] = __builtin_fmaf(d[r], s, acc[t][r]);
+    }
+  }
+}
+
+// Rows row0 .. row0 + rows - 1 (at most 16 NT) of expert e by columns n0 .. n0 + 15.
+template <int FW, int FA, typename O, int NT, int KS>
+__device__ __forceinline__ void few_rows(const muon_product_args& p, int e, int row0, int rows, int64_t n0, int part,
+                                         float (*sums)[64][16]) {
+  constexpr int U = NT == 1 ? 4 : 2;
+  const int lane = threadIdx.x & 63, g = lane >> 4, q = lane & 15;
+  const int64_t KB = (p.k + 127) / 128, NB = (p.n + 127) / 128;
+  const uint8_t* w = static_cast<const uint8_t*>(p.w) + (int64_t)e * p.w_matrix + min(n0 + q, p.n - 1) * p.w_stride;
+  const float* ws = p.w_scales + ((int64_t)e * NB + n0 / 128) * KB;
+  const uint8_t* a[NT];
+  const float* as[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int64_t r = row0 + min(16 * t + q, rows - 1);
+    a[t] = static_cast<const uint8_t*>(p.a) + r * p.a_stride;
+    as[t] = p.a_scales + r * p.a_scales_stride;
+  }
+  f32x4 acc[NT] = {};
+  const int64_t full = p.k / (128 * U) * U;   // blocks in whole groups
+  for (int64_t b = part * U; b < full; b += KS * U)
+    few_blocks<FW, FA, O, NT, U, true>(w, a, ws, as, b, KB, p.k, acc);
+  if (full < KB && full / U % KS == part)      // the rest is one group at most
+    few_blocks<FW, FA, O, NT, U, false>(w, a, ws, as, full, KB, p.k, acc);
+  if (KS > 1) {
+    __syncthreads();   // the sums of the rows before have been read
+    if (part > 0) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(&sums[part][lane][4 * t]) = acc[t];
+    }
+    __syncthreads();
+    if (part > 0) return;
+#pragma unroll
+    for (int s = 1; s < KS; ++s)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[t] += *reinterpret_cast<const f32x4*>(&sums[s][lane][4 * t]);
+  }
+  const int64_t n = n0 + 4 * g;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+    if (16 * t + q < rows && n < p.n)
+      store4<O>(static_cast<O*>(p.out) + (int64_t)(row0 + 16 * t + q) * p.out_stride, n, p.n, acc[t]);
+}
+
+template <int FW, int FA, typename O, int KS>
+__global__ void __launch_bounds__(KS > 4 ? 64 * KS : 256)
+ex_product_few(muon_product_args p) {
+  constexpr int TILES = KS > 4 ? 1 : 4 / KS;   // of 16 columns a workgroup
+  __shared__ float sums[KS > 1 ? TILES * KS : 1][64][16];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tile = wave / KS, part = wave % KS;
+  for (int e = blockIdx.y; e < (int)p.num_experts; e += gridDim.y) {
+    int lo, hi;
+    run_of(p.offsets, e, (int)p.rows, lo, hi);
+    for (int64_t x = blockIdx.x; lo < hi && x * TILES * 16 < p.n; x += gridDim.x) {
+      // a wave past the last column works on that column's tile again (its sums' barriers are everyone's)
+      const int64_t n0 = min((x * TILES + tile) * 16, (p.n - 1) / 16 * 16);
+      for (int r = lo; r < hi; r += 64) {
+        const int rows = min(hi - r, 64);
+        if (rows <= 16) few_rows<FW, FA, O, 1, KS>(p, e, r, rows, n0, part, sums + tile * KS);
+        else if (rows <= 32) few_rows<FW, FA, O, 2, KS>(p, e, r, rows, n0, part, sums + tile * KS);
+        else few_rows<FW, FA, O, 4, KS>(p, e, r, rows, n0, part, sums + tile * KS);
+      }
+    }
+  }
+}
+
+template <int FW, int FA, typename O, int KS>
+hipError_t launch_few(const muon_product_args& p, hipStream_t stream) {
+  constexpr int TILES = KS > 4 ? 1 : 4 / KS;
+  const int64_t x = (p.n + TILES * 16 - 1) / (TILES * 16);
+  ex_product_few<FW, FA, O, KS><<<dim3(unsigned(x < (1 << 20) ? x : 1 << 20), unsigned(p.num_experts)),
+                                 KS > 4 ? 64 * KS : 256, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
 // Rows in 16-byte pieces at 16-byte addresses, with a tile's offsets in 32 bits.
 bool whole_pieces(const muon_product_args& p) {
   auto fine = [&](const void* base, int64_t stride) {
@@ -436,9 +576,21 @@ bool whole_pieces(const muon_product_args& p) {
 
 template <int FW, int FA, typename O>
 hipError_t launch(const muon_product_args& p, hipStream_t stream) {
+  const bool tiled = sizeof(O) == 2 && whole_pieces(p) && p.k > 128;
+  const int64_t experts = p.num_experts < p.rows ? p.num_experts : p.rows, wide = (p.n + kTile - 1) / kTile;
+  // Few rows an expert: with 8 rows for each of 64 [4096, 7168] 368 us by single waves and 425 by tiles of 256,
+  // with 16 448 and 430.  Where the tiles leave CUs without one, also with more: one [4096, 7168] with 64 rows 23
+  // and 59 us, one [8192, 28672] 158 and 215, with 96 rows 250 and 220.
+  if (p.rows <= (tiled && experts * wide >= 128 ? 8 : 64) * p.num_experts && p.rows < (1 << 30)) {
+    // waves for all 1024 SIMDs four times over, or the blocks of k shared by up to eight
+    const int64_t tiles = (p.n + 15) / 16 * experts, blocks = (p.k + 127) / 128;
+    const int64_t share = tiles >= 4096 || blocks < 8 ? 1 : tiles >= 1024 || blocks < 32 ? 4 : 8;
+    return share == 1 ? launch_few<FW, FA, O, 1>(p, stream) : share == 4 ? launch_few<FW, FA, O, 4>(p, stream)
+                                                                         : launch_few<FW, FA, O, 8>(p, stream);
+  }
   if constexpr (sizeof(O) == 2) {
-    if (whole_pieces(p) && p.k > 128) {
-      ex_product_tiled<FW, FA><<<256, 512, 0, stream>>>(p, (uint32_t)((p.n + kTile - 1) / kTile));
+    if (tiled) {
+      ex_product_tiled<FW, FA><<<256, 512, 0, stream>>>(p, (uint32_t)wide);
       return hipGetLastError();
     }
   }
