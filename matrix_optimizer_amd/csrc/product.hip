@@ -102,7 +102,7 @@ __device__ __forceinline__ void store4<float>(float* row, int64_t n, int64_t N, 
 // alignment, through registers.  The matrices' rows are the instruction's
 // first operand, so that a lane ends with four neighbouring columns of one row.
 template <int FW, int FA, typename O>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 2)
 ex_product(muon_product_args p, uint32_t tiles_n) {
   typedef Block<FW, FA, O> Blk;
   constexpr int BM = 128, BN = 128;
@@ -126,16 +126,26 @@ ex_product(muon_product_args p, uint32_t tiles_n) {
       as[j] = p.a_scales + (int64_t)(tile.row0 + (live[j] ? r : 0)) * p.a_scales_stride;
     }
     f32x4 acc[4][4] = {};
+    // Rows 32 i + t / 8 of W, then of A, piece t % 8; those past the end repeat the last.
     u32x4 v[8];
-    auto load = [&](int64_t b) {
+    const uint8_t* from[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = (t >> 3) + 32 * i, c = t & 7;   // rows 0 .. 127 of W, then of A
-        v[i] = u32x4{};
-        if (i < 4) {
-          if (n0 + r < p.n) v[i] = load16(W + r * p.w_stride, b * 128 + c * 16, p.k);
-        } else {
-          if (r - BN < tile.rows) v[i] = load16(A + (int64_t)(r - BN) * p.a_stride, b * 128 + c * 16, p.k);
+    for (int i = 0; i < 8; ++i) {
+      const int r = (t >> 3) + 32 * (i & 3);
+      from[i] = i < 4 ? W + min((int64_t)r, p.n - 1 - n0) * p.w_stride : A + (int64_t)min(r, tile.rows - 1) * p.a_stride;
+    }
+    auto load = [&](int64_t b) {
+      const int64_t k = b * 128 + (t & 7) * 16;
+      if (b * 128 + 128 <= p.k) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const u32x4_any*>(from[i] + k);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const u32x4 x = load16(from[i], k, p.k);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (i == j) v[j] = x;
         }
       }
     };
@@ -151,19 +161,23 @@ ex_product(muon_product_args p, uint32_t tiles_n) {
       __syncthreads();
       if (b + 1 < KB) load(b + 1);
       const float sw = ws[b];
-      typename Blk::Frag fw[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) fw[i] = Blk::template make<FW>(fragment(stage, wn * 64 + i * 16 + q, g));
+      typename Blk::Frag fa[4];
+      float s[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const typename Blk::Frag fa = Blk::template make<FA>(fragment(stage, BN + wm * 64 + j * 16 + q, g));
-        const float s = live[j] ? as[j][b] * sw : 0.f;
+        fa[j] = Blk::template make<FA>(fragment(stage, BN + wm * 64 + j * 16 + q, g));
+        s[j] = as[j][b] * sw;
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f32x4 d = Blk::mfma(fw[i], fa);
+      for (int i = 0; i < 4; ++i) {   // one fragment of W at a time: as bf16 they are large
+        const typename Blk::Frag fw = Blk::template make<FW>(fragment(stage, wn * 64 + i * 16 + q, g));
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[r], s, acc[i][j][r]);
+        for (int j = 0; j < 4; ++j) {
+          const f32x4 d = Blk::mfma(fw, fa[j]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[r], s[j], acc[i][j][r]);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
 #pragma unroll
