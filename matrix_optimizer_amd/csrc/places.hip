@@ -17,15 +17,15 @@ __device__ __forceinline__ void copy_row(const uint8_t* src, uint8_t* dst, int64
     return;
   }
   const int64_t n = (width + 15) >> 4;
-  for (int64_t c = first + lane; c < n; c += 4 * step) {
-    u32x4_any v[4];
+  for (int64_t c = first + lane; c < n; c += 8 * step) {
+    u32x4_any v[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       const int64_t o = (c + j * step) * 16;
       if (c + j * step < n) v[j] = *reinterpret_cast<const u32x4_any*>(src + (o + 16 <= width ? o : width - 16));
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       const int64_t o = (c + j * step) * 16;
       if (c + j * step < n) *reinterpret_cast<u32x4_any*>(dst + (o + 16 <= width ? o : width - 16)) = v[j];
     }
@@ -90,64 +90,82 @@ ex_combine(muon_combine_args a, int log_lanes) {
 }
 
 // ---------------------------------------------------------------------------
-// combine's gradients, a wave or a workgroup (LANES) for each row of dout.
+// combine's gradients, LANES lanes for each row of dout, four slots at a time:
+// their rows of y are on their way together, and dout is read once for them.
+// Few rows have their slots dealt to several workgroups (grid.y).
 // ---------------------------------------------------------------------------
 template <typename T, int LANES>
 __global__ void __launch_bounds__(256)
 ex_combine_backward(muon_combine_grad_args a) {
-  __shared__ float dots[4][32];
-  constexpr int PER = 256 / LANES;
+  constexpr int PER = 256 / LANES, SLOTS = 4;
+  __shared__ float dots[4][SLOTS];
   const int lane = threadIdx.x & (LANES - 1), wave = threadIdx.x / WAVE;
   const int K = (int)a.top_k;
   const bool e5 = a.dy8_dtype == MUON_ROW_E5M2;
   const int64_t steps = (a.cols + LANES * 8 - 1) / (LANES * 8);
   for (int64_t t0 = (int64_t)blockIdx.x * PER; t0 < a.rows; t0 += (int64_t)gridDim.x * PER) {
     const int64_t t = t0 + threadIdx.x / LANES;
-    if (t < a.rows) {
-      const T* dout = static_cast<const T*>(a.dout) + t * a.dout_stride;
-      for (int k = 0; k < K; ++k) {
-        const int64_t i = a.position[t * K + k];
-        float dot = 0.f;
-        if (i >= 0 && i < a.places) {
-          const float w = a.weights ? a.weights[t * K + k] : 1.f;
-          for (int64_t s = 0; s < steps; ++s) {
-            const int64_t c = (s * LANES + lane) * 8;   // may pass the row's end: a group's lanes stay together
-            float d[8], f[8];
-            load8(dout, c, a.cols, d);
-            if (a.dweights) {
-              load8(static_cast<const T*>(a.y) + i * a.y_stride, c, a.cols, f);
+    for (int k0 = blockIdx.y * SLOTS; k0 < K; k0 += gridDim.y * SLOTS) {
+      float dot[SLOTS] = {};
+      if (t < a.rows) {
+        const T* dout = static_cast<const T*>(a.dout) + t * a.dout_stride;
+        int64_t at[SLOTS];
+        float w[SLOTS];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) dot = __builtin_fmaf(d[e], f[e], dot);
+        for (int j = 0; j < SLOTS; ++j) {
+          const int64_t p = t * K + min(k0 + j, K - 1), i = a.position[p];
+          at[j] = k0 + j < K && i >= 0 && i < a.places ? i : -1;
+          w[j] = a.weights ? a.weights[p] : 1.f;
+        }
+        for (int64_t s = 0; s < steps; ++s) {
+          const int64_t c = (s * LANES + lane) * 8;   // may pass the row's end: a group's lanes stay together
+          float d[8], f[8];
+          Chunk<T> y[SLOTS], x;
+          x.load(dout, c, a.cols);
+          if (a.dweights) {
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j)
+              if (at[j] >= 0) y[j].load(static_cast<const T*>(a.y) + at[j] * a.y_stride, c, a.cols);
+          }
+          x.get(d, c, a.cols);
+          // the group's largest |w d| is |w| times its largest |d|: rounding keeps the order
+          const float most = a.dy8 ? over_row<16>(most8(d), max_f) : 0.f;
+#pragma unroll
+          for (int j = 0; j < SLOTS; ++j) {
+            if (at[j] < 0) continue;
+            if (a.dweights) {
+              y[j].get(f, c, a.cols);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) dot[j] = __builtin_fmaf(d[e], f[e], dot[j]);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] *= w;
-            if (a.dy && c < a.cols) store8(static_cast<T*>(a.dy) + i * a.dy_stride, c, a.cols, d);
-            if (a.dy8) {
-              const float scale = group_scale(over_row<16>(most8(d), max_f), e5);
-              if (c < a.cols) {
-                if ((c & 127) == 0) a.scales[i * a.scales_stride + (c >> 7)] = scale;
-                store_eight(static_cast<uint8_t*>(a.dy8) + i * a.dy8_stride, c, a.cols, d, scale, e5);
-              }
+            for (int e = 0; e < 8; ++e) f[e] = d[e] * w[j];
+            if (a.dy && c < a.cols) store8(static_cast<T*>(a.dy) + at[j] * a.dy_stride, c, a.cols, f);
+            if (a.dy8 && c < a.cols) {
+              const float scale = group_scale(fmaxf(most * fabsf(w[j]), 0.f), e5);   // NaN: no product but NaN, or zeros
+              if ((c & 127) == 0) a.scales[at[j] * a.scales_stride + (c >> 7)] = scale;
+              store_eight(static_cast<uint8_t*>(a.dy8) + at[j] * a.dy8_stride, c, a.cols, f, scale, e5);
             }
           }
         }
         if (a.dweights) {
-          dot = over_row<WAVE>(dot, add_f);
-          if (LANES == WAVE) {
-            if (lane == 0) a.dweights[t * K + k] = dot;
-          } else if ((threadIdx.x & (WAVE - 1)) == 0) {
-            dots[wave][k] = dot;
+#pragma unroll
+          for (int j = 0; j < SLOTS; ++j) {
+            dot[j] = over_row<(LANES < WAVE ? LANES : WAVE)>(dot[j], add_f);
+            if (LANES <= WAVE && lane == 0 && k0 + j < K) a.dweights[t * K + k0 + j] = dot[j];
           }
         }
       }
-    }
-    if (LANES > WAVE && a.dweights) {
-      __syncthreads();
-      if ((int)threadIdx.x < K && t < a.rows) {
-        const int k = threadIdx.x;
-        a.dweights[t * K + k] = (dots[0][k] + dots[1][k]) + (dots[2][k] + dots[3][k]);
+      if (LANES > WAVE && a.dweights) {   // t is the workgroup's
+        if ((threadIdx.x & (WAVE - 1)) == 0) {
+#pragma unroll
+          for (int j = 0; j < SLOTS; ++j) dots[wave][j] = dot[j];
+        }
+        __syncthreads();
+        const int j = threadIdx.x;
+        if (j < SLOTS && k0 + j < K) a.dweights[t * K + k0 + j] = (dots[0][j] + dots[1][j]) + (dots[2][j] + dots[3][j]);
+        __syncthreads();
       }
-      __syncthreads();
     }
   }
 }
@@ -159,23 +177,29 @@ hipError_t combine_to(const muon_combine_args& a, const RowLayout& l, hipStream_
   return hipGetLastError();
 }
 
+template <typename T, int LANES>
+hipError_t launch_backward(const muon_combine_grad_args& a, hipStream_t stream) {
+  constexpr int PER = 256 / LANES;
+  const int64_t groups = (a.rows + PER - 1) / PER, most = 1 << 20, sets = (a.top_k + 3) / 4;
+  const int64_t y = groups >= 512 ? 1 : sets;
+  ex_combine_backward<T, LANES><<<dim3(unsigned(groups < most ? groups : most), unsigned(y)), 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
 template <typename T>
 hipError_t combine_backward_of(const muon_combine_grad_args& a, hipStream_t stream) {
-  const int64_t most = 1 << 20;
-  if (a.cols <= 1024) {
-    const int64_t groups = (a.rows + 3) / 4;
-    ex_combine_backward<T, 64><<<unsigned(groups < most ? groups : most), 256, 0, stream>>>(a);
-  } else {
-    ex_combine_backward<T, 256><<<unsigned(a.rows < most ? a.rows : most), 256, 0, stream>>>(a);
-  }
-  return hipGetLastError();
+  if (a.cols <= 256) return launch_backward<T, 32>(a, stream);
+  return a.cols <= 1024 ? launch_backward<T, 64>(a, stream) : launch_backward<T, 256>(a, stream);
 }
 
 }  // namespace
 
 hipError_t run_gather(const muon_gather_args& a, hipStream_t stream) {
   const int64_t es = a.dtype == MUON_ROW_F32 ? 4 : a.dtype == MUON_ROW_BF16 ? 2 : 1;
-  const RowLayout l = row_layout(a.rows * a.top_k, (a.cols * es + 15) / 16);
+  // Many rows: at most a wave each, with up to eight pieces a lane on their way (49152 rows of 7168 bytes
+  // and their scales 104 us; a workgroup each 128).
+  const int64_t pairs = a.rows * a.top_k, chunks = (a.cols * es + 15) / 16;
+  const RowLayout l = row_layout(pairs, pairs >= 4096 && chunks > 64 ? 64 : chunks);
   ex_gather<<<dim3(l.gx, l.gy), 256, 0, stream>>>(a, es, l.log_lanes);
   return hipGetLastError();
 }

@@ -28,7 +28,7 @@ __device__ __forceinline__ u32x4 load8_bf16(const bf16_t* row, int64_t c, int64_
 }
 
 // ---------------------------------------------------------------------------
-// 128 x 128 of one expert's matrix a workgroup, 64 x 64 a wave, 32 rows a
+// 128 x 128 of one expert's matrix a workgroup, 64 x 64 a wave, 64 rows a
 // step: both operands lie with the rows of the sum along the slow axis, so
 // their fragments are read transposed.  Any size, stride and alignment,
 // through registers.
@@ -36,8 +36,8 @@ __device__ __forceinline__ u32x4 load8_bf16(const bf16_t* row, int64_t c, int64_
 template <typename O>
 __global__ void __launch_bounds__(256)
 ex_weight_grad(muon_weight_grad_args p, Dest d, int64_t tn, int64_t tk) {
-  constexpr int BK = 32;
-  __shared__ u32x4 lds[2][BK][16];   // rows of 128 columns of dy and of x
+  constexpr int BK = 64, N = BK / 16;
+  __shared__ u32x4 lds[2][2][BK][16];   // twice rows of 128 columns of dy and of x, piece c of row r in slot c ^ 4 (r % 4)
   const int t = threadIdx.x, lane = t & 63, w = t >> 6, wn = w & 1, wk = w >> 1;
   for (int64_t index = blockIdx.x; index < p.num_experts * tn * tk * d.parts; index += gridDim.x) {
     const int part = (int)(index % d.parts);
@@ -48,22 +48,42 @@ ex_weight_grad(muon_weight_grad_args p, Dest d, int64_t tn, int64_t tk) {
     run_of(p.offsets, e, (int)p.rows, lo, hi);
     part_of(part, d.parts, 64, lo, hi);
     f32x16 acc[2][2] = {};
-    for (int64_t r0 = lo; r0 < hi; r0 += BK) {
-      __syncthreads();
+    // the next step's pieces in registers while a step is multiplied: rows t / 16 and N - 1 times 16 more,
+    // piece t % 16; rows past the run's end are zeros
+    u32x4 v[2][N];
+    const int r = t >> 4, c = t & 15;
+    const bool whole = n0 + 128 <= p.n && k0 + 128 <= p.k;
+    auto load = [&](int64_t r0) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = (t >> 4) + 16 * i, c = t & 15;
-        u32x4 a = {}, b = {};
-        if (r0 + r < hi) {
-          a = load8_bf16(static_cast<const bf16_t*>(p.dy) + (r0 + r) * p.dy_stride, n0 + c * 8, p.n);
-          b = load8_bf16(static_cast<const bf16_t*>(p.x) + (r0 + r) * p.x_stride, k0 + c * 8, p.k);
+      for (int i = 0; i < N; ++i) {
+        v[0][i] = v[1][i] = u32x4{};
+        const int64_t at = r0 + r + 16 * i;
+        if (at >= hi) continue;
+        const bf16_t* dy = static_cast<const bf16_t*>(p.dy) + at * p.dy_stride;
+        const bf16_t* x = static_cast<const bf16_t*>(p.x) + at * p.x_stride;
+        if (whole) {
+          v[0][i] = *reinterpret_cast<const u32x4_any*>(dy + n0 + c * 8);
+          v[1][i] = *reinterpret_cast<const u32x4_any*>(x + k0 + c * 8);
+        } else {
+          v[0][i] = load8_bf16(dy, n0 + c * 8, p.n);
+          v[1][i] = load8_bf16(x, k0 + c * 8, p.k);
         }
-        lds[0][r][c] = a;
-        lds[1][r][c] = b;
+      }
+    };
+    load(lo);
+    __syncthreads();   // the tile before has been multiplied
+    int turn = 0;
+    for (int64_t r0 = lo; r0 < hi; r0 += BK, turn ^= 1) {
+      // written while others still multiply the step before from the other half
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        lds[turn][0][r + 16 * i][c ^ (4 * (r & 3))] = v[0][i];
+        lds[turn][1][r + 16 * i][c ^ (4 * (r & 3))] = v[1][i];
       }
       __syncthreads();
-      const bf16_t* A = reinterpret_cast<const bf16_t*>(lds[0]);
-      const bf16_t* B = reinterpret_cast<const bf16_t*>(lds[1]);
+      load(r0 + BK);
+      const bf16_t* A = reinterpret_cast<const bf16_t*>(lds[turn][0]);
+      const bf16_t* B = reinterpret_cast<const bf16_t*>(lds[turn][1]);
       const int G = lane >> 4, s4 = lane & 15;
 #pragma unroll
       for (int kk = 0; kk < BK / 16; ++kk) {
@@ -77,7 +97,7 @@ ex_weight_grad(muon_weight_grad_args p, Dest d, int64_t tn, int64_t tk) {
             for (int hh = 0; hh < 2; ++hh) {
               const int row = 16 * kk + 8 * (G >> 1) + 4 * hh + (s4 >> 2);
               const int col = (op ? wk : wn) * 64 + i * 32 + 16 * (G & 1) + 4 * (s4 & 3);
-              h[hh] = lds_read_tr16((op ? B : A) + row * 128 + col);
+              h[hh] = lds_read_tr16((op ? B : A) + row * 128 + ((((col >> 3) ^ (4 * (row & 3))) << 3) | (col & 7)));
             }
             f[op][i] = __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7);
           }
@@ -356,12 +376,19 @@ ex_weight_grad_join(muon_weight_grad_args p, const float* parts, int n_parts, in
   const int64_t chunks = (p.k + 7) / 8, all = p.num_experts * p.n * chunks;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
     const int64_t row = i / chunks, c = (i - row * chunks) * 8, e = row / p.n, n = row - e * p.n;
-    float s[8], f[8];
-    load8(parts + row * p.k, c, p.k, s);
-    for (int j = 1; j < n_parts; ++j) {
-      load8(parts + j * part + row * p.k, c, p.k, f);
+    float s[8] = {}, f[8];
+    for (int j = 0; j < n_parts; j += 8) {   // eight parts on their way together
+      Chunk<float> v[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) s[q] += f[q];
+      for (int u = 0; u < 8; ++u)
+        if (j + u < n_parts) v[u].load(parts + (j + u) * part + row * p.k, c, p.k);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (j + u >= n_parts) continue;
+        v[u].get(f, c, p.k);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s[q] += f[q];
+      }
     }
     store8(static_cast<O*>(p.dw) + e * p.dw_matrix + n * p.dw_stride, c, p.k, s);
   }
