@@ -91,7 +91,8 @@ muon_status muon_expert_combine(const muon_combine_args* args, void* stream);
  *   dweights[t, k] = sum over columns of dout[t] y[i] (optional, needs y),
  * and dweights = 0 for a slot without one.  Places that no slot names are
  * left as they are.  The places are distinct, as muon_route_order gives them;
- * of a place named twice one slot's row stays.  The gradient of base is dout. */
+ * a place named twice holds either slot's value in each column.  The gradient
+ * of base is dout. */
 typedef struct {
   int64_t rows, cols, top_k, places;
   const int32_t* position;                           /* [rows, top_k], contiguous */
@@ -166,7 +167,8 @@ muon_status muon_quantise_blocks(const muon_quantise_args* args, void* stream);
  * sums over a block are fp32 sums of exact products; with bf16 out the 8-bit
  * instructions form them, which cut each of eight neighbouring products at
  * 2^-13 of the largest one's power of two.  offsets NULL: one expert, all rows.
- * num_experts <= MUON_ROUTE_MAX_EXPERTS. */
+ * num_experts <= MUON_ROUTE_MAX_EXPERTS, and fewer than 2^31 pieces of out of
+ * 128 x 128 in the runs. */
 typedef struct {
   int64_t rows, n, k, num_experts;
   const void* a;        int64_t a_stride;               /* [rows, k] of a_dtype */
@@ -185,7 +187,7 @@ muon_status muon_expert_product(const muon_product_args* args, void* stream);
  * one expert, all rows.  rows = 0 writes zeros.  num_experts <=
  * MUON_ROUTE_MAX_EXPERTS.  The workspace (256-byte
  * aligned) is that of muon_expert_weight_grad_workspace_bytes, 0 bytes where
- * the rows are not split. */
+ * the rows are not split; it serves one call at a time. */
 typedef struct {
   int64_t rows, n, k, num_experts;
   const void* dy;       int64_t dy_stride;              /* [rows, n] bf16 */

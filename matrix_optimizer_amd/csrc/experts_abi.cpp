@@ -198,6 +198,9 @@ muon_status muon_expert_product(const muon_product_args* a, void* stream) {
   if ((st = check_groups(a->rows, a->num_experts, a->offsets)) != MUON_OK) return st;
   if (!eight_bit(a->a_dtype) || !eight_bit(a->w_dtype) || !valid_dtype(a->out_dtype)) return MUON_ERR_INVALID_ARG;
   if (too_many(a->num_experts, a->n, a->k)) return MUON_ERR_UNSUPPORTED;
+  // tiles are numbered in 32 bits
+  if ((a->rows / 128 + (a->num_experts < a->rows ? a->num_experts : a->rows)) * blocks_of(a->n) >= (int64_t(1) << 31))
+    return MUON_ERR_UNSUPPORTED;
   if (a->rows == 0) return MUON_OK;
   const int64_t kb = blocks_of(a->k);
   Buffers b;

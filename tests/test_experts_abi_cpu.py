@@ -163,6 +163,7 @@ def test_product_refusals(mem):
     _refused(call, (dict(rows=1 << 31), dict(n=1 << 31), dict(k=1 << 31), dict(num_experts=1025),
                     dict(num_experts=1024, n=1 << 30, k=1 << 30)), UNSUPPORTED)
     assert call(rows=0, a=None) == OK
+    _refused(call, (dict(rows=(1 << 31) - 1, n=(1 << 31) - 1, k=1, w_stride=1, num_experts=1),), UNSUPPORTED)   # too many tiles
     assert call() == call(num_experts=1, offsets=None, w_matrix=0) == HIP
 
 
