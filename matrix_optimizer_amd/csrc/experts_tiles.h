@@ -48,6 +48,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int experts, i
       const uint32_t own = __builtin_amdgcn_readlane(tm, at), end = __builtin_amdgcn_readlane(sum, at);
       const uint32_t local = index - (before + end - own * tiles_n);
       const uint32_t n = __builtin_amdgcn_readfirstlane(local / own), m = local - n * own;
+      if (n >= tiles_n) return false;   // overlapping runs of more tiles than 32 bits number
       t.e = e0 + at;
       t.tn = (int)n;
       t.row0 = __builtin_amdgcn_readlane(lo, at) + (int)m * bm;
