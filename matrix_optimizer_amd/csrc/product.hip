@@ -113,9 +113,12 @@ ex_product(muon_product_args p, uint32_t tiles_n) {
   __shared__ u32x4 lds[2][(BM + BN) * 8];
   const int t = threadIdx.x, lane = t & 63, g = lane >> 4, q = lane & 15, w = t >> 6, wn = w & 1, wm = w >> 1;
   const int64_t KB = (p.k + 127) / 128, NB = (p.n + 127) / 128;
+  // consecutive tiles, which share their operands, to the workgroups of one XCD (every eighth)
+  const uint32_t total = count_tiles(p.offsets, (int)p.num_experts, (int)p.rows, BM, tiles_n), per = (total + 7) / 8;
+  const uint32_t end = min(total, (blockIdx.x & 7) * per + per);
   ExpertTile tile;
-  for (uint32_t index = blockIdx.x;
-       find_tile(p.offsets, (int)p.num_experts, (int)p.rows, BM, tiles_n, index, tile); index += gridDim.x) {
+  for (uint32_t index = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+       index < end && find_tile(p.offsets, (int)p.num_experts, (int)p.rows, BM, tiles_n, index, tile); index += gridDim.x >> 3) {
     const int64_t n0 = (int64_t)tile.tn * BN;
     const uint8_t* W = static_cast<const uint8_t*>(p.w) + (int64_t)tile.e * p.w_matrix + n0 * p.w_stride;
     const uint8_t* A = static_cast<const uint8_t*>(p.a) + (int64_t)tile.row0 * p.a_stride;
@@ -625,7 +628,7 @@ hipError_t launch(const muon_product_args& p, hipStream_t stream) {
   }
   const int64_t tiles_n = (p.n + 127) / 128;
   const int64_t most = (p.rows / 128 + (p.num_experts < p.rows ? p.num_experts : p.rows)) * tiles_n;
-  ex_product<FW, FA, O><<<unsigned(most < (1 << 20) ? most : 1 << 20), 256, 0, stream>>>(p, (uint32_t)tiles_n);
+  ex_product<FW, FA, O><<<unsigned(most < (1 << 20) ? (most + 7) / 8 * 8 : 1 << 20), 256, 0, stream>>>(p, (uint32_t)tiles_n);
   return hipGetLastError();
 }
 

@@ -40,10 +40,15 @@ ex_weight_grad(muon_weight_grad_args p, Dest d, int64_t tn, int64_t tk) {
   constexpr int BK = 64, N = BK / 16;
   __shared__ u32x4 lds[2][2][BK][16];   // twice rows of 128 columns of dy and of x, piece c of row r in slot c ^ 4 (r % 4)
   const int t = threadIdx.x, lane = t & 63, w = t >> 6, wn = w & 1, wk = w >> 1;
-  for (int64_t index = blockIdx.x; index < p.num_experts * tn * tk * d.parts; index += gridDim.x) {
-    const int part = (int)(index % d.parts);
-    const int64_t tile = index / d.parts, jk = tile % tk, jn = tile / tk % tn;
-    const int e = (int)(tile / (tk * tn));
+  // an expert's tiles, which share their operands, dealt in eight runs to the XCDs as below
+  const int64_t each = tn * tk * d.parts, xcd = blockIdx.x & 7;
+  const bool deal = each >= 64;
+  const int64_t from = deal ? each * xcd / 8 : 0, mine = deal ? each * (xcd + 1) / 8 - from : each;
+  for (int64_t index = deal ? blockIdx.x >> 3 : blockIdx.x; index < mine * p.num_experts;
+       index += deal ? gridDim.x >> 3 : gridDim.x) {
+    const int e = (int)(index / mine);
+    const int64_t local = from + index - e * mine, tile = local / d.parts, jk = tile % tk, jn = tile / tk;
+    const int part = (int)(local % d.parts);
     const int64_t n0 = jn * 128, k0 = jk * 128;
     int lo, hi;
     run_of(p.offsets, e, (int)p.rows, lo, hi);
@@ -416,7 +421,7 @@ hipError_t launch(const muon_weight_grad_args& p, const Dest& d, hipStream_t str
     ex_weight_grad_tiled<O><<<256, 512, 0, stream>>>(p, d, (uint32_t)tn, (uint32_t)tk);
   } else {
     const int64_t sn = (p.n + 127) / 128, sk = (p.k + 127) / 128, tiles = p.num_experts * sn * sk * d.parts;
-    ex_weight_grad<O><<<unsigned(tiles < (1 << 20) ? tiles : 1 << 20), 256, 0, stream>>>(p, d, sn, sk);
+    ex_weight_grad<O><<<unsigned(tiles < (1 << 20) ? (tiles + 7) / 8 * 8 : 1 << 20), 256, 0, stream>>>(p, d, sn, sk);
   }
   return hipGetLastError();
 }
