@@ -102,9 +102,10 @@ __device__ __forceinline__ void store4<float>(float* row, int64_t n, int64_t N, 
 // alignment, through registers, a block ahead of the one multiplied.  The
 // matrices' rows are the instruction's first operand, so that a lane ends with
 // four neighbouring columns of one row.  3001 rows by 13 of 16 [1371, 2051] to
-// fp32: 61 us, 267 TFLOP/s (144 without the loads ahead, 98 with one workgroup a
-// CU); 49152 rows by 64 [2048, 4096] to fp32 630 TFLOP/s.  Bound by its two
-// workgroups a CU and, to fp32, by the conversions.
+// fp32: 59 us, 277 TFLOP/s (144 without the loads ahead, 98 with one workgroup a
+// CU); 49152 rows by 64 [2048, 4096] to fp32 671 TFLOP/s (630 with neighbouring
+// tiles on different XCDs).  Bound by its two workgroups a CU and, to fp32, by the
+// conversions.
 template <int FW, int FA, typename O>
 __global__ void __launch_bounds__(256, 2)
 ex_product(muon_product_args p, uint32_t tiles_n) {
