@@ -187,7 +187,7 @@ muon_status muon_expert_product(const muon_product_args* args, void* stream);
  * one expert, all rows.  rows = 0 writes zeros.  num_experts <=
  * MUON_ROUTE_MAX_EXPERTS.  The workspace (256-byte
  * aligned) is that of muon_expert_weight_grad_workspace_bytes, 0 bytes where
- * the rows are not split; it serves one call at a time. */
+ * the rows are neither split nor of odd widths; it serves one call at a time. */
 typedef struct {
   int64_t rows, n, k, num_experts;
   const void* dy;       int64_t dy_stride;              /* [rows, n] bf16 */

@@ -223,8 +223,8 @@ muon_status muon_expert_weight_grad_workspace_bytes(int64_t rows, int64_t num_ex
   if (num_experts < 1) return MUON_ERR_INVALID_ARG;
   if (num_experts > MUON_ROUTE_MAX_EXPERTS) return MUON_ERR_UNSUPPORTED;
   if (too_many(num_experts, n, k)) return MUON_ERR_UNSUPPORTED;
-  const int64_t parts = weight_grad_parts(rows, num_experts, n, k);
-  *out = parts > 1 ? align256(size_t(parts) * size_t(num_experts * n * k) * 4) : 0;
+  *out = align256(size_t(weight_grad_parts_bytes(rows, num_experts, n, k)) +
+                  size_t(weight_grad_copy_bytes(rows, num_experts, n, k)));
   return MUON_OK;
 }
 
@@ -246,7 +246,7 @@ muon_status muon_expert_weight_grad(const muon_weight_grad_args* a, void* worksp
   stack(b, a->dw, a->num_experts, a->n, a->k, a->dw_stride, a->dw_matrix, size_of(a->dw_dtype), true);
   if (need) b.flat(workspace, int64_t(need), 1, true, 256);
   if ((st = b.check()) != MUON_OK) return st;
-  return hip_status(run_weight_grad(*a, static_cast<float*>(workspace), hip_stream(stream)));
+  return hip_status(run_weight_grad(*a, workspace, hip_stream(stream)));
 }
 
 }  // extern "C"

@@ -31,9 +31,8 @@ __device__ __forceinline__ u32x4 load8_bf16(const bf16_t* row, int64_t c, int64_
 // step: both operands lie with the rows of the sum along the slow axis, so
 // their fragments are read transposed.  Any size, stride and alignment,
 // through registers, a step ahead of the one multiplied.  777 rows of 1001 and 515
-// columns for 8 experts 16-20 us; 49152 rows of 1001 and 1001 for 8 experts 0.52
-// ms, 190 TFLOP/s, of 1024 and 1024 0.28: bound by loads that start at any element,
-// eight times over.
+// columns for 8 experts 16-20 us, bound by latency; 49152 rows of 1001 and 1001 for 8
+// experts took 0.52 ms and of 1024 and 1024 0.28, by loads that start at any element.
 // ---------------------------------------------------------------------------
 template <typename O>
 __global__ void __launch_bounds__(256)
@@ -130,7 +129,7 @@ ex_weight_grad(muon_weight_grad_args p, Dest d, int64_t tn, int64_t tk) {
 
 // ---------------------------------------------------------------------------
 // 256 x 256 a workgroup of eight waves, 64 (n) x 128 (k) a wave, for rows of
-// whole 16-byte pieces.
+// whole 16-byte pieces (those of the last columns may be filled up).
 //
 // 64 rows of both operands at a time come straight from global memory into one
 // of two stages; a wave multiplies a stage in four steps of 16 rows, eight
@@ -173,6 +172,26 @@ __device__ __forceinline__ void whole_rows(u32x4 (&r)[4]) {
   swap_lanes16(r[1], r[3]);
 }
 
+// 16 bytes of a row, of which `left` elements belong to it.
+__device__ __forceinline__ void store_piece(bf16_t* p, int left, const u32x4& v) {
+  if (left >= 8) {
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(p));
+  } else {
+#pragma unroll
+    for (int r = 0; r < 7; ++r)
+      if (r < left) p[r] = (bf16_t)(v[r >> 1] >> (16 * (r & 1)));
+  }
+}
+__device__ __forceinline__ void store_piece(float* p, int left, const u32x4& v) {
+  if (left >= 4) {
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(p));
+  } else {
+#pragma unroll
+    for (int r = 0; r < 3; ++r)
+      if (r < left) p[r] = __uint_as_float(v[r]);
+  }
+}
+
 // 32 rows of 64 (bf16) or 32 (fp32) columns from an accumulator pair or one accumulator; `k_left` columns and
 // `n_left` rows belong to the matrix.
 __device__ __forceinline__ void store_rows(bf16_t* out, int64_t stride, int k_left, int n_left, const f32x16& v0, const f32x16& v1) {
@@ -194,7 +213,7 @@ __device__ __forceinline__ void store_rows(bf16_t* out, int64_t stride, int k_le
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     const int n = 8 * s + (lane & 7);
-    if (k < k_left && n < n_left) __builtin_nontemporal_store(r[s], reinterpret_cast<u32x4_any*>(out + n * stride + k));   // columns are whole pieces
+    if (n < n_left) store_piece(out + n * stride + k, k_left - k, r[s]);
   }
 }
 __device__ __forceinline__ void store_rows(float* out, int64_t stride, int k_left, int n_left, const f32x16& v) {
@@ -208,7 +227,7 @@ __device__ __forceinline__ void store_rows(float* out, int64_t stride, int k_lef
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     const int n = 8 * s + (lane & 7);
-    if (k < k_left && n < n_left) __builtin_nontemporal_store(r[s], reinterpret_cast<u32x4_any*>(out + n * stride + k));
+    if (n < n_left) store_piece(out + n * stride + k, k_left - k, r[s]);
   }
 }
 
@@ -268,9 +287,9 @@ ex_weight_grad_tiled(muon_weight_grad_args p, Dest d, uint32_t tn, uint32_t tk) 
     if (!live) return Rows64{buffer_of(p.dy, 0), buffer_of(p.x, 0), 0, 0};
     const int left = load.hi - first, n = left < kRows ? left : kRows;
     const Rows64 r{buffer_of(static_cast<const bf16_t*>(p.dy) + (int64_t)first * p.dy_stride + load.n0,
-                             n > 0 ? (n - 1) * d_pitch + (uint32_t)(p.n - load.n0) * 2 : 0),
+                             n > 0 ? (n - 1) * d_pitch + (uint32_t)((p.n + 7) / 8 * 8 - load.n0) * 2 : 0),
                    buffer_of(static_cast<const bf16_t*>(p.x) + (int64_t)first * p.x_stride + load.k0,
-                             n > 0 ? (n - 1) * x_pitch + (uint32_t)(p.k - load.k0) * 2 : 0),
+                             n > 0 ? (n - 1) * x_pitch + (uint32_t)((p.k + 7) / 8 * 8 - load.k0) * 2 : 0),
                    first, load.hi};
     first += kRows;
     if (first >= load.hi) {
@@ -406,19 +425,41 @@ ex_weight_grad_join(muon_weight_grad_args p, const float* parts, int n_parts, in
   }
 }
 
+// Rows of dy (y = 0) and x (y = 1) copied to rows of whole 16-byte pieces, zeros behind the last column.
+__global__ void __launch_bounds__(256)
+ex_weight_grad_align(muon_weight_grad_args p, bf16_t* dy, bf16_t* x) {
+  const bool second = blockIdx.y != 0;
+  const int64_t cols = second ? p.k : p.n, chunks = (cols + 7) / 8, stride = second ? p.x_stride : p.dy_stride;
+  const bf16_t* from = static_cast<const bf16_t*>(second ? p.x : p.dy);
+  bf16_t* to = second ? x : dy;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.rows * chunks; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / chunks, c = (i - r * chunks) * 8;
+    Chunk<bf16_t> v;
+    v.load(from + r * stride, c, cols);
+    v.settle(c, cols);
+    *reinterpret_cast<u32x4*>(to + i * 8) = v.v;
+  }
+}
+
+// A tile's row and column numbers fit 32 bits with room for the tile.
+bool numbers_fit(int64_t rows, int64_t experts, int64_t n, int64_t k, int64_t parts) {
+  const int64_t most = int64_t(1) << 22;
+  return rows > 0 && rows < (1 << 30) && n < most && k < most &&
+         experts * ((n + kTile - 1) / kTile) * ((k + kTile - 1) / kTile) * parts < (int64_t(1) << 31);
+}
+
+// 16-byte addresses and strides, and whole pieces.
 bool whole_pieces(const muon_weight_grad_args& p) {
   auto fine = [&](const void* base, int64_t stride, int64_t cols) {
     return reinterpret_cast<uintptr_t>(base) % 16 == 0 && cols % 8 == 0 && (p.rows <= 1 || stride % 8 == 0) && stride < (1 << 22);
   };
-  // a tile's row and column numbers fit 32 bits with room for the tile
-  return p.rows > 0 && p.rows < (1 << 30) && p.n < (1 << 30) && p.k < (1 << 30) && fine(p.dy, p.dy_stride, p.n) &&
-         fine(p.x, p.x_stride, p.k);
+  return fine(p.dy, p.dy_stride, p.n) && fine(p.x, p.x_stride, p.k);
 }
 
 template <typename O>
-hipError_t launch(const muon_weight_grad_args& p, const Dest& d, hipStream_t stream) {
+hipError_t launch(const muon_weight_grad_args& p, const Dest& d, bool pieces, hipStream_t stream) {
   const int64_t tn = (p.n + kTile - 1) / kTile, tk = (p.k + kTile - 1) / kTile;
-  if (whole_pieces(p) && p.num_experts * tn * tk * d.parts < (int64_t(1) << 31)) {
+  if (pieces) {
     ex_weight_grad_tiled<O><<<256, 512, 0, stream>>>(p, d, (uint32_t)tn, (uint32_t)tk);
   } else {
     const int64_t sn = (p.n + 127) / 128, sk = (p.k + 127) / 128, tiles = p.num_experts * sn * sk * d.parts;
@@ -440,14 +481,39 @@ int64_t weight_grad_parts(int64_t rows, int64_t num_experts, int64_t n, int64_t 
   return parts < 2 ? 1 : parts;
 }
 
-hipError_t run_weight_grad(const muon_weight_grad_args& p, float* parts, hipStream_t stream) {
+// Odd widths of 2^30 products or more have their rows copied to whole pieces first: 49152 rows of 1001 and 1001
+// for 8 experts 248 us, 515 without, 4096 rows of 1001 and 515 45 and 61, 2000 of them 34 and 33, 777 24 and 15.
+int64_t weight_grad_copy_bytes(int64_t rows, int64_t num_experts, int64_t n, int64_t k) {
+  if (n % 8 == 0 && k % 8 == 0) return 0;
+  if (!numbers_fit(rows, num_experts, n, k, weight_grad_parts(rows, num_experts, n, k)) || rows * n < (int64_t(1) << 30) / k) return 0;
+  return rows * ((n + 7) / 8 + (k + 7) / 8) * 16;
+}
+
+hipError_t run_weight_grad(const muon_weight_grad_args& args, void* workspace, hipStream_t stream) {
+  muon_weight_grad_args p = args;
   const int64_t n_parts = weight_grad_parts(p.rows, p.num_experts, p.n, p.k), part = p.num_experts * p.n * p.k;
   const bool f32 = p.dw_dtype == MUON_F32;
+  float* parts = static_cast<float*>(workspace);
+  bool pieces = numbers_fit(p.rows, p.num_experts, p.n, p.k, n_parts);
+  if (weight_grad_copy_bytes(p.rows, p.num_experts, p.n, p.k)) {
+    p.dy_stride = (p.n + 7) / 8 * 8;
+    p.x_stride = (p.k + 7) / 8 * 8;
+    bf16_t* dy = reinterpret_cast<bf16_t*>(static_cast<uint8_t*>(workspace) + weight_grad_parts_bytes(p.rows, p.num_experts, p.n, p.k));
+    bf16_t* x = dy + p.rows * p.dy_stride;
+    const int64_t wide = p.n > p.k ? p.n : p.k, need = (p.rows * ((wide + 7) / 8) + 255) / 256;
+    ex_weight_grad_align<<<dim3(unsigned(need < (1 << 16) ? need : 1 << 16), 2), 256, 0, stream>>>(args, dy, x);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    p.dy = dy;
+    p.x = x;
+  } else {
+    pieces = pieces && whole_pieces(p);
+  }
   if (n_parts == 1) {
     const Dest d{p.dw, p.dw_stride, p.dw_matrix, 0, 1};
-    return f32 ? launch<float>(p, d, stream) : launch<bf16_t>(p, d, stream);
+    return f32 ? launch<float>(p, d, pieces, stream) : launch<bf16_t>(p, d, pieces, stream);
   }
-  const hipError_t err = launch<float>(p, Dest{parts, p.k, p.n * p.k, part, (int)n_parts}, stream);
+  const hipError_t err = launch<float>(p, Dest{parts, p.k, p.n * p.k, part, (int)n_parts}, pieces, stream);
   if (err != hipSuccess) return err;
   const int64_t blocks = (p.num_experts * p.n * ((p.k + 7) / 8) + 255) / 256;
   const unsigned grid = unsigned(blocks < (1 << 16) ? blocks : 1 << 16);

@@ -102,6 +102,31 @@ def test_weight_gradients_of_split_rows(counts, n, k):
             within(dw[i], d.T @ v, okind, (hi - lo + 64) * 2 * U * (d.abs().T @ v.abs()), i)
 
 
+@pytest.mark.parametrize("n,k,okind", [(1001, 707, "bf16"), (1001, 712, "f32"), (1000, 715, "bf16"), (333, 2049, "f32")])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (5, 3)])
+def test_weight_gradients_of_odd_widths(n, k, okind, pad, shift):
+    """Widths that are no whole pieces, with work enough that the rows are copied to such first."""
+    counts = [5000, 0, 2100, 1]
+    g = torch.Generator(device="cuda").manual_seed(n + k)
+    offsets = offsets_of(counts)
+    live = int(offsets[-1])
+    r = live + 70
+    need = X.expert_weight_grad_workspace_bytes(r, 4, n, k)
+    assert need >= 2 * r * (n + k)
+    dy, x = (torch.randn(r, c + pad, generator=g, device="cuda").bfloat16()[:, shift:shift + c] for c in (n, k))
+    dy[live:], x[live:] = float("nan"), float("inf")
+    full = torch.full((4, n + 1, k + pad), 7.0, device="cuda").to(T[okind])
+    dw = full[:, :n, shift:shift + k]
+    ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    X.muon_expert_weight_grad(dy, x, dw, offsets=torch.from_numpy(offsets).cuda(), workspace=ws[:need])
+    for i, (lo, hi) in enumerate(zip(offsets, offsets[1:])):
+        d, v = dy[lo:hi].double(), x[lo:hi].double()
+        within(dw[i], d.T @ v, okind, (hi - lo + 64) * 2 * U * (d.abs().T @ v.abs()), i)
+    edge = full.float().clone()
+    edge[:, :n, shift:shift + k] = 7
+    assert bool((edge == 7).all()) and bool((ws[need:] == 0xFF).all())
+
+
 def test_products_repeat_bitwise():
     """The same call twice, with other work on the card in between: the same bits."""
     g = torch.Generator(device="cuda").manual_seed(1)
