@@ -57,20 +57,32 @@ __device__ __forceinline__ void lds_dma16(const void* base, uint32_t voff, uint3
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :: "v"(voff), "s"(sb), "s"(sl) : "memory", "m0");
 }
-// The same from a buffer of `bytes` bytes at a uniform offset beyond the lane's own; what lies past the
-// buffer's end is not read (and what arrives for it is of no use).
+// The same from a buffer of `bytes` bytes: lanes whose offset lies past its end read nothing (and what arrives
+// for them is of no use).  The scalar offset is 0, so that the lane's offset alone is compared with the size.
 __device__ __forceinline__ u32x4 buffer_of(const void* base, uint32_t bytes) {
   const uint64_t b = (uint64_t)uniform64((int64_t)(uintptr_t)base);
   return u32x4{(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, (uint32_t)__builtin_amdgcn_readfirstlane(bytes), 0x00020000u};
 }
+// A buffer that begins `bytes` bytes later and ends where it did.
+__device__ __forceinline__ void advance(u32x4& buffer, uint32_t bytes) {
+  const uint64_t b = ((uint64_t)buffer[1] << 32 | buffer[0]) + bytes;
+  buffer[0] = (uint32_t)b;
+  buffer[1] = (uint32_t)(b >> 32);
+  buffer[2] -= bytes;
+}
+__device__ __forceinline__ void lds_dma16(const u32x4& buffer, uint32_t voff, uint32_t lds_addr) {
+  const uint32_t sl = __builtin_amdgcn_readfirstlane(lds_addr);
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               :: "v"(voff), "s"(buffer), "s"(sl) : "memory", "m0");
+}
+__device__ __forceinline__ void lds_dma4(const u32x4& buffer, uint32_t voff, uint32_t lds_addr) {
+  const uint32_t sl = __builtin_amdgcn_readfirstlane(lds_addr);
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               :: "v"(voff), "s"(buffer), "s"(sl) : "memory", "m0");
+}
 __device__ __forceinline__ void lds_dma16(const u32x4& buffer, uint32_t voff, uint32_t soff, uint32_t lds_addr) {
   const uint32_t so = __builtin_amdgcn_readfirstlane(soff), sl = __builtin_amdgcn_readfirstlane(lds_addr);
   asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-               :: "v"(voff), "s"(buffer), "s"(so), "s"(sl) : "memory", "m0");
-}
-__device__ __forceinline__ void lds_dma4(const u32x4& buffer, uint32_t voff, uint32_t soff, uint32_t lds_addr) {
-  const uint32_t so = __builtin_amdgcn_readfirstlane(soff), sl = __builtin_amdgcn_readfirstlane(lds_addr);
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
                :: "v"(voff), "s"(buffer), "s"(so), "s"(sl) : "memory", "m0");
 }
 // The same with 4 bytes per lane, to lds_addr + 4 lane.

@@ -2,6 +2,7 @@
 // a[i, k] w[e, n, k] with a scale for each block of 128 of k.
 #include "experts_tiles.h"
 #include "lds.h"
+#include "stages.h"
 
 namespace muon {
 namespace {
@@ -227,20 +228,22 @@ __device__ __forceinline__ void store_packed8(bf16_t* p, int left, const u32x4& 
 // whole block old, are there, so that the last part reads the first fragments of
 // the next block and no wave finds itself without operands.
 //
-// 49152 rows by 64 [4096, 7168] 1.54-1.58 ms, 1800 TFLOP/s of useful products at
+// 49152 rows by 64 [4096, 7168] 1.57-1.61 ms, 1770 TFLOP/s of useful products at
 // 2.0 GHz; the matrix units are busy for 45 % of it.  Without any load the same
 // kernel takes 1.24 ms, with all loads from the L2 and no products 0.77, with all
 // loads and no products 1.57: it is bound by how many lines a CU has on their way,
 // 64 KB a block.  Fetching lines towards the L2 one to six blocks ahead takes their
-// place (1.57 to 1.72 ms).  Two wave groups a quarter block apart with four barriers a
+// place (1.57 to 1.72 ms).  With the rows in the loads' scalar offset, which the
+// hardware need not compare with a buffer's end, runs of whole tiles took 1.47 ms
+// for 1.48.  Two wave groups a quarter block apart with four barriers a
 // block took 1.80 ms, address arithmetic in the vector unit 1.72.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 256, kStage = 2 * kTile * 128 + kTile * 4 + 256;
 
-// A tile's operands as buffers that end with its last row, and where its rows' and columns' scales begin.
+// A tile's operands, and the scales that a wave loads, as buffers from the next block to load on; they end with
+// the tile's last row.
 struct Operands {
-  u32x4 w, a;
-  uint32_t as, ws;
+  u32x4 w, a, scales;
 };
 
 __device__ __forceinline__ u32x4 lds_read16(uint32_t at) {
@@ -280,34 +283,40 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
   if (index >= end || !find_tile(runs, E, rows, kTile, tiles_n, index, tile)) return;
 
   const uint32_t w_pitch = (uint32_t)p.w_stride, a_pitch = (uint32_t)p.a_stride, s_pitch = (uint32_t)p.a_scales_stride * 4u;
-  const u32x4 as_all = buffer_of(p.a_scales, (rows - 1) * s_pitch + KB * 4), ws_all = buffer_of(p.w_scales, E * NB * KB * 4);
   auto operands = [&](const ExpertTile& x) {
     const ArgsPtr p = args_again();
     const int64_t n0 = (int64_t)x.tn * kTile;
-    const int wl = (int)min((int64_t)kTile, p->n - n0) - 1, al = x.rows - 1;
-    return Operands{buffer_of(static_cast<const uint8_t*>(p->w) + (int64_t)x.e * p->w_matrix + n0 * p->w_stride, wl * w_pitch + K),
-                    buffer_of(static_cast<const uint8_t*>(p->a) + (int64_t)x.row0 * p->a_stride, al * a_pitch + K),
-                    (uint32_t)x.row0 * s_pitch, (uint32_t)(x.e * NB + 2 * x.tn) * KB * 4};
+    const uint32_t wr = (uint32_t)min((int64_t)kTile, p->n - n0), ar = x.rows;
+    return Operands{
+        buffer_of(static_cast<const uint8_t*>(p->w) + (int64_t)x.e * p->w_matrix + n0 * p->w_stride, product_bytes(wr, w_pitch, K, 0)),
+        buffer_of(static_cast<const uint8_t*>(p->a) + (int64_t)x.row0 * p->a_stride, product_bytes(ar, a_pitch, K, 0)),
+        w < 4 ? buffer_of(p->a_scales + (int64_t)x.row0 * p->a_scales_stride, product_bytes(ar, s_pitch, KB * 4, 0))
+              : buffer_of(p->w_scales + ((int64_t)x.e * NB + 2 * x.tn) * KB, product_bytes(wr > 128 ? 2 : 1, KB * 4, KB * 4, 0))};
   };
-  // Block kb of a tile to a stage, load `part` of nine: this wave's 32 rows of each operand, eight a
+  // The next block of a tile to a stage, load `part` of nine: this wave's 32 rows of each operand, eight a
   // load, 16-byte piece c of row r in slot slot_of(r, c), then scales.  Pieces past the end of a row are
   // cleared by settle().
-  auto piece_of = [](int l, int j) { return ((l & 7) ^ ((4 * j + (l >> 4)) & 7)) * 16; };
-  const uint32_t row = 32 * w + (lane >> 3);
-  const uint32_t w_off[2] = {row * w_pitch + piece_of(lane, 0), row * w_pitch + piece_of(lane, 1)};
-  const uint32_t a_off[2] = {row * a_pitch + piece_of(lane, 0), row * a_pitch + piece_of(lane, 1)};
-  const uint32_t s_off = w < 4 ? (64 * w + lane) * s_pitch : (lane & 1) * KB * 4;
-  auto issue = [&](const Operands& o, int kb, uint32_t stage, int part) {
+  uint32_t w_off[4], a_off[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    w_off[j] = product_offset(w, lane, j, w_pitch);
+    a_off[j] = product_offset(w, lane, j, a_pitch);
+  }
+  const uint32_t s_off = w < 4 ? product_scale_offset(w, lane, s_pitch) : product_matrix_scale_offset(lane, KB * 4);
+  auto issue = [&](const Operands& o, uint32_t stage, int part) {
     if (part < 8) {
       const int j = part >> 1;
       const uint32_t to = stage + w * 4096 + j * 1024;
-      if (part & 1) lds_dma16(o.a, a_off[j & 1], kb * 128 + 8 * j * a_pitch, to + kTile * 128);
-      else lds_dma16(o.w, w_off[j & 1], kb * 128 + 8 * j * w_pitch, to);
-    } else if (w < 4) {
-      lds_dma4(as_all, s_off, o.as + kb * 4, stage + 2 * kTile * 128 + w * 256);
-    } else if (w == 4) {
-      lds_dma4(ws_all, s_off, o.ws + kb * 4, stage + 2 * kTile * 128 + kTile * 4);
+      if (part & 1) lds_dma16(o.a, a_off[j], to + kTile * 128);
+      else lds_dma16(o.w, w_off[j], to);
+    } else if (w <= 4) {   // the matrix's behind the rows'
+      lds_dma4(o.scales, s_off, stage + 2 * kTile * 128 + w * 256);
     }
+  };
+  auto block_on = [&](Operands& o) {
+    advance(o.w, 128);
+    advance(o.a, 128);
+    advance(o.scales, 4);
   };
   // this wave's loads have arrived, block kb's in the given stage
   bool stores = false;
@@ -320,7 +329,7 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
       asm volatile("" : "+v"(l));
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (kb * 128 + piece_of(l, j) >= K) {
+        if (kb * 128 + (int)product_piece(l, j) >= K) {
           u32x4* to = reinterpret_cast<u32x4*>(lds + (stage - lds0) + w * 4096 + l * 16 + j * 1024);
           to[0] = u32x4{};
           to[kTile * 8] = u32x4{};
@@ -332,12 +341,14 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
     return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
   };
 
-  Operands cur = operands(tile);
+  Operands at = operands(tile);
   uint32_t here = lds0, there = lds0 + kStage;
 #pragma unroll
-  for (int x = 0; x < 9; ++x) issue(cur, 0, here, x);
+  for (int x = 0; x < 9; ++x) issue(at, here, x);
+  block_on(at);
 #pragma unroll
-  for (int x = 0; x < 9; ++x) issue(cur, 1, there, x);
+  for (int x = 0; x < 9; ++x) issue(at, there, x);
+  block_on(at);
   settle(0, here);
   lds_barrier();
   // this lane's addresses in a stage
@@ -363,28 +374,25 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
     ExpertTile next = tile;   // the last tile loads its own first blocks once more
     index += step;
     more = index < end && find_tile(runs, E, rows, kTile, tiles_n, index, next);
-    const Operands then = operands(next);
     if (wm * 64 >= tile.rows) {   // on a short last tile one wave of each SIMD only loads
       for (int kb = 0; kb < KB; ++kb) {
         settle(kb + 1 < KB ? kb + 1 : 0, there);
         lds_barrier();
-        const bool ahead = kb + 2 < KB;
+        if (kb + 2 == KB) at = operands(next);
 #pragma unroll
-        for (int x = 0; x < 9; ++x) issue(ahead ? cur : then, ahead ? kb + 2 : kb + 2 - KB, here, x);
+        for (int x = 0; x < 9; ++x) issue(at, here, x);
+        block_on(at);
         const uint32_t x = here;
         here = there;
         there = x;
       }
       first_fragments(here);
       tile = next;
-      cur = then;
       continue;
     }
     f32x4 acc[8][4] = {};
     for (int kb = 0; kb < KB; ++kb) {
-      const bool ahead = kb + 2 < KB;
-      const int nb = ahead ? kb + 2 : kb + 2 - KB;
-      const Operands& of = ahead ? cur : then;
+      if (kb + 2 == KB) at = operands(next);
       float s[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[j] = sn[j] * swn;
@@ -413,10 +421,11 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
           if (x < 26) fw[0][x - 24] = read(there + wlo + (x - 24) * 2048, there + whi + (x - 24) * 2048);
           if (x & 1) fa[j] = read(there + alo + j * 2048, there + ahi + j * 2048);
           else sn[j] = lds_read4(there + sat + j * 64);
-          issue(of, nb, here, x - 24);
+          issue(at, here, x - 24);
         } else if (x == 32) {
           swn = lds_read4(there + swat);
-          issue(of, nb, here, 8);
+          issue(at, here, 8);
+          block_on(at);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -458,7 +467,6 @@ ex_product_tiled(muon_product_args p, uint32_t tiles_n) {
     // sixteen stores, and nothing else, behind the loads that settle() waits for next
     stores = n_left == 128 && r_left >= 64;
     tile = next;
-    cur = then;
   }
   // the loads that are still on their way go to this workgroup's memory
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
