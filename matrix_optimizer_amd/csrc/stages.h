@@ -29,4 +29,15 @@ constexpr uint32_t product_bytes(uint32_t rows, uint32_t pitch, uint32_t width, 
 constexpr uint32_t product_scale_offset(int wave, int lane, uint32_t pitch) { return (64u * wave + lane) * pitch; }
 constexpr uint32_t product_matrix_scale_offset(int lane, uint32_t pitch) { return (lane & 1) * pitch; }
 
+// Weight gradient: 64 rows of 512 bytes (256 columns) an operand, eight rows a wave in four loads of two rows.
+// 16-byte piece c of row r lies in slot c ^ 4 (r % 4).
+constexpr uint32_t grad_row(int wave, int lane, int load) { return 8u * wave + 2u * load + (lane >> 5); }
+constexpr uint32_t grad_piece(int lane, int load) { return ((lane & 31) ^ (4 * (lane >> 5) + 8 * (load & 1))) * 16; }
+constexpr uint32_t grad_offset(int wave, int lane, int load, uint32_t pitch) {
+  return grad_row(wave, lane, load) * pitch + grad_piece(lane, load);
+}
+// Bytes from a tile's first column in the stage's first row to the end of the last of `rows` rows (none for rows
+// <= 0), which have `left` bytes from that column on.
+constexpr uint32_t grad_bytes(int rows, uint32_t pitch, uint32_t left) { return rows > 0 ? (rows - 1) * pitch + left : 0; }
+
 }  // namespace muon

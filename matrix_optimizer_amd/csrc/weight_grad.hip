@@ -2,6 +2,7 @@
 // expert's rows, bf16 products summed in fp32.
 #include "experts_tiles.h"
 #include "lds.h"
+#include "stages.h"
 
 namespace muon {
 namespace {
@@ -142,7 +143,7 @@ ex_weight_grad(muon_weight_grad_args p, Dest d, int64_t tn, int64_t tk) {
 // instruction's rows, so that a lane ends with runs of four along k, eight after
 // one exchange with the lane 32 away.
 //
-// 49152 rows to 64 [7168, 2048] bf16 1.47-1.51 ms, 930 TFLOP/s; a stage takes
+// 49152 rows to 64 [7168, 2048] bf16 1.47-1.52 ms, 930 TFLOP/s; a stage takes
 // 1.8 us (as in the 8-bit product the lines that a CU has on their way, 64 KB a
 // stage), the matrix units are busy for 47 % of it, and the 1.9 GB of results take
 // 0.24 ms that no products hide.
@@ -271,10 +272,12 @@ ex_weight_grad_tiled(muon_weight_grad_args p, Dest d, uint32_t tn, uint32_t tk) 
   // piece c of row r in slot c ^ 4 (r % 4), so that the four rows of a transposing read lie on different
   // banks.  The buffers end with the run; rows past it are cleared by settle().
   const uint32_t d_pitch = (uint32_t)p.dy_stride * 2, x_pitch = (uint32_t)p.x_stride * 2;
-  auto lane_off = [&](uint32_t pitch, int j) {   // rows 2 j + (lane >> 5), j even / odd
-    return (lane >> 5) * pitch + (uint32_t)((lane & 31) ^ (4 * (lane >> 5) + 8 * j)) * 16;
-  };
-  const uint32_t d_off[2] = {lane_off(d_pitch, 0), lane_off(d_pitch, 1)}, x_off[2] = {lane_off(x_pitch, 0), lane_off(x_pitch, 1)};
+  uint32_t d_off[4], x_off[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    d_off[j] = grad_offset(w, lane, j, d_pitch);
+    x_off[j] = grad_offset(w, lane, j, x_pitch);
+  }
   Tile load = tile_at(index);       // the tile being loaded, its next rows, whether there are any
   uint32_t load_index = index;
   int first = load.lo;
@@ -287,9 +290,9 @@ ex_weight_grad_tiled(muon_weight_grad_args p, Dest d, uint32_t tn, uint32_t tk) 
     if (!live) return Rows64{buffer_of(p.dy, 0), buffer_of(p.x, 0), 0, 0};
     const int left = load.hi - first, n = left < kRows ? left : kRows;
     const Rows64 r{buffer_of(static_cast<const bf16_t*>(p.dy) + (int64_t)first * p.dy_stride + load.n0,
-                             n > 0 ? (n - 1) * d_pitch + (uint32_t)((p.n + 7) / 8 * 8 - load.n0) * 2 : 0),
+                             grad_bytes(n, d_pitch, (uint32_t)((p.n + 7) / 8 * 8 - load.n0) * 2)),
                    buffer_of(static_cast<const bf16_t*>(p.x) + (int64_t)first * p.x_stride + load.k0,
-                             n > 0 ? (n - 1) * x_pitch + (uint32_t)((p.k + 7) / 8 * 8 - load.k0) * 2 : 0),
+                             grad_bytes(n, x_pitch, (uint32_t)((p.k + 7) / 8 * 8 - load.k0) * 2)),
                    first, load.hi};
     first += kRows;
     if (first >= load.hi) {
@@ -303,8 +306,8 @@ ex_weight_grad_tiled(muon_weight_grad_args p, Dest d, uint32_t tn, uint32_t tk) 
   auto issue = [&](const Rows64& r, uint32_t stage, int part) {   // load `part` of eight
     const int j = part >> 1;
     const uint32_t to = stage + w * 4096 + j * 1024;
-    if (part & 1) lds_dma16(r.x, x_off[j & 1], (8 * w + 2 * j) * x_pitch, to + kStage / 2);
-    else lds_dma16(r.dy, d_off[j & 1], (8 * w + 2 * j) * d_pitch, to);
+    if (part & 1) lds_dma16(r.x, x_off[j], to + kStage / 2);
+    else lds_dma16(r.dy, d_off[j], to);
   };
   constexpr int kStores = sizeof(O) == 2 ? 16 : 32;
   bool stores = false;   // a tile's stores, and nothing else, are behind the loads that settle() waits for

@@ -65,6 +65,31 @@ int main() {
 }
 """
 
+GRAD = """
+int main() {
+  const uint32_t widths[] = {8, 16, 128, 248, 256, 264, 512, 1000};
+  for (uint32_t cols : widths)
+    for (uint32_t pitch : {2 * cols, 2 * cols + 16, (1u << 23) - 16})
+      for (uint32_t first = 0; first < cols; first += 256)      // the tile's first column
+        for (int rows = -3; rows <= 64; ++rows) {
+          const uint32_t left = (cols - first) * 2, bytes = grad_bytes(rows, pitch, left);
+          CHECK(rows > 0 ? 2 * first + bytes == uint64_t(rows - 1) * pitch + 2 * cols : bytes == 0);
+          for (int w = 0; w < 8; ++w)
+            for (int lane = 0; lane < 64; ++lane)
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t r = grad_row(w, lane, j), c = grad_piece(lane, j);
+                const uint64_t off = uint64_t(r) * pitch + c;
+                CHECK(grad_offset(w, lane, j, pitch) == off);                 // no carry out of 32 bits
+                CHECK(w * 4096 + j * 1024 + lane * 16 == int(r * 512 + ((c / 16) ^ (4 * (r & 3))) * 16));
+                if (int(r) >= rows) CHECK(off >= bytes);                      // not read
+                else if (c < left) CHECK(off + 16 <= bytes);                  // read whole
+                else if (off < bytes) CHECK(off + 16 <= bytes);               // another row's, within the run
+              }
+        }
+  std::puts("ok");
+}
+"""
+
 
 def run(body, tmp_path):
     src, exe = tmp_path / "reach.cpp", tmp_path / "reach"
@@ -80,6 +105,10 @@ def test_product_tiles_stay_within_their_operands(tmp_path):
     run(PRODUCT, tmp_path)
 
 
+def test_weight_gradient_tiles_stay_within_their_operands(tmp_path):
+    run(GRAD, tmp_path)
+
+
 def test_product_loads_have_no_scalar_offset():
     """The kernel's lane offsets and buffers are those checked above, and its loads take nothing besides them."""
     src = open(os.path.join(CSRC, "product.hip")).read()
@@ -88,3 +117,13 @@ def test_product_loads_have_no_scalar_offset():
     assert src.count("lds_dma") == 3
     forms = [line for line in open(os.path.join(CSRC, "lds.h")) if "buffer_load_dword " in line]
     assert forms and all("%0, %1, 0 offen lds" in line for line in forms)
+
+
+def test_weight_gradient_loads_have_no_scalar_offset():
+    src = open(os.path.join(CSRC, "weight_grad.hip")).read()
+    for call in ("lds_dma16(r.x, x_off[j], ", "lds_dma16(r.dy, d_off[j], "):
+        assert call in src
+    assert src.count("lds_dma") == 2
+    for name in os.listdir(CSRC):
+        forms = [line for line in open(os.path.join(CSRC, name)) if "buffer_load_dword" in line]
+        assert all("%0, %1, 0 offen lds" in line for line in forms), name
