@@ -73,6 +73,20 @@ __device__ __forceinline__ uint32_t count_tiles(const int32_t* offsets, int expe
   return __builtin_amdgcn_readfirstlane(sum);
 }
 
+// Where the last run ends: rows from there on belong to nobody.  Every lane of a wave takes part.
+__device__ __forceinline__ int end_of_runs(const int32_t* offsets, int experts, int rows) {
+  if (!offsets) return rows;
+  int end = 0;
+  for (int e = threadIdx.x & (WAVE - 1); e < experts; e += WAVE) {
+    int lo, hi;
+    run_of(offsets, e, rows, lo, hi);
+    if (lo < hi) end = max(end, hi);
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) end = max(end, __shfl_xor(end, d, WAVE));
+  return __builtin_amdgcn_readfirstlane(end);
+}
+
 // Bytes k .. k+15 of a row of K bytes, zeros from K on (k may lie past it).
 __device__ __forceinline__ u32x4 load16(const uint8_t* row, int64_t k, int64_t K) {
   if (k + 16 <= K) return *reinterpret_cast<const u32x4_any*>(row + k);

@@ -428,14 +428,16 @@ ex_weight_grad_join(muon_weight_grad_args p, const float* parts, int n_parts, in
   }
 }
 
-// Rows of dy (y = 0) and x (y = 1) copied to rows of whole 16-byte pieces, zeros behind the last column.
+// Rows of dy (y = 0) and x (y = 1) up to the end of the runs, copied to rows of whole 16-byte pieces, zeros
+// behind the last column.
 __global__ void __launch_bounds__(256)
 ex_weight_grad_align(muon_weight_grad_args p, bf16_t* dy, bf16_t* x) {
   const bool second = blockIdx.y != 0;
   const int64_t cols = second ? p.k : p.n, chunks = (cols + 7) / 8, stride = second ? p.x_stride : p.dy_stride;
   const bf16_t* from = static_cast<const bf16_t*>(second ? p.x : p.dy);
   bf16_t* to = second ? x : dy;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.rows * chunks; i += (int64_t)gridDim.x * 256) {
+  const int64_t all = end_of_runs(p.offsets, (int)p.num_experts, (int)p.rows) * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / chunks, c = (i - r * chunks) * 8;
     Chunk<bf16_t> v;
     v.load(from + r * stride, c, cols);

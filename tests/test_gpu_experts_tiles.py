@@ -127,6 +127,49 @@ def test_weight_gradients_of_odd_widths(n, k, okind, pad, shift):
     assert bool((edge == 7).all()) and bool((ws[need:] == 0xFF).all())
 
 
+@pytest.mark.parametrize("n,k", [(1001, 1003), (1001, 712), (1000, 1005)])
+def test_weight_gradients_of_odd_widths_leave_rows_without_a_run(n, k):
+    """Rows behind the last run are not copied either: the copies' places for them in the workspace keep what they
+    held.  16 experts are enough tiles, so that the workspace holds the copies alone: dy's, then x's."""
+    counts = [90] * 15 + [113]
+    offsets = offsets_of(counts)
+    live = int(offsets[-1])
+    r = live + 301
+    g = torch.Generator(device="cuda").manual_seed(n + k)
+    wide = [-(-c // 8) * 8 for c in (n, k)]
+    need = X.expert_weight_grad_workspace_bytes(r, 16, n, k)
+    assert need == -(-2 * r * sum(wide) // 256) * 256
+    dy, x = (torch.randn(r, c, generator=g, device="cuda").bfloat16() for c in (n, k))
+    dw = torch.full((16, n, k), 7.0, device="cuda")
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    X.muon_expert_weight_grad(dy, x, dw, offsets=torch.from_numpy(offsets).cuda(), workspace=ws)
+    at = 0
+    for c, of in zip(wide, (dy, x)):
+        rows = ws[at:at + 2 * r * c].view(r, 2 * c)
+        copied = rows[:live].view(torch.bfloat16)[:, :of.shape[1]]
+        assert torch.equal(copied, of[:live]) and bool((rows[live:] == 0xFF).all())
+        at += 2 * r * c
+    for i, (lo, hi) in enumerate(zip(offsets, offsets[1:])):
+        d, v = dy[lo:hi].double(), x[lo:hi].double()
+        within(dw[i], d.T @ v, "f32", (hi - lo + 16) * 2 * U * (d.abs().T @ v.abs()), i)
+
+
+def test_weight_gradients_of_odd_widths_and_bad_offsets():
+    """Runs out of order and offsets outside the rows: the copies reach to the end of the furthest run."""
+    n, k, r = 1001, 1003, 1500
+    g = torch.Generator(device="cuda").manual_seed(3)
+    dy, x = (torch.randn(r, c, generator=g, device="cuda").bfloat16() for c in (n, k))
+    ws = torch.full((X.expert_weight_grad_workspace_bytes(r, 3, n, k),), 0xFF, dtype=torch.uint8, device="cuda")
+    assert ws.numel() >= 2 * r * (n + k)
+    for offsets in ([700, 1400, 30, 200], [-7, 600, 600, 1 << 30], [0, 0, 0, -2**31], [1499, 1500, 1500, 3]):
+        dw = torch.full((3, n, k), 7.0, device="cuda")
+        X.muon_expert_weight_grad(dy, x, dw, offsets=torch.tensor(offsets, dtype=torch.int32, device="cuda"), workspace=ws)
+        at = [min(max(v, 0), r) for v in offsets]
+        for i, (lo, hi) in enumerate(zip(at, at[1:])):
+            d, v = dy[lo:max(lo, hi)].double(), x[lo:max(lo, hi)].double()
+            within(dw[i], d.T @ v, "f32", (max(hi - lo, 0) + 64) * 2 * U * (d.abs().T @ v.abs()), (offsets, i))
+
+
 def test_products_repeat_bitwise():
     """The same call twice, with other work on the card in between: the same bits."""
     g = torch.Generator(device="cuda").manual_seed(1)
