@@ -100,6 +100,26 @@ def test_product_runs(counts):
     product_case(rng, counts, 128, 528, okind="f32", tail=5)
 
 
+@pytest.mark.parametrize("okind", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [4096, 4133, 7168])
+@pytest.mark.parametrize("rows", [1, 16, 33, 64])
+def test_product_of_few_rows_by_eight_waves(rows, k, okind):
+    """One matrix with few columns and long rows: eight waves share the blocks of k."""
+    rng = np.random.default_rng(rows * 10007 + k)
+    product_case(rng, [rows], 40, k, okind=okind)
+    product_case(rng, [rows - 1, 1], 35, k, "e5m2", "e4m3", okind, tail=2, pad=5, shift=3)
+
+
+@pytest.mark.parametrize("counts,n,k,okind", [
+    ([600] + [0] * 8 + [2], 96, 4224, "f32"), ([0] * 4 + [300] + [0] * 3 + [290, 1], 48, 4100, "f32"),                # eight waves
+    ([0] * 60 + [300] + [0] * 60 + [600, 3, 0, 65], 272, 1040, "bf16"), ([700] + [1] * 20, 80, 1024, "f32"),    # four
+    ([0] * 60 + [257] + [0] * 70 + [513], 272, 256, "bf16"), ([1, 640, 0, 320] + [0] * 12, 64, 384, "f32")])    # one
+def test_product_of_long_runs_among_few_rows(counts, n, k, okind):
+    """Few rows an expert in the mean, but runs of several times 256: the workgroups of a run take several turns."""
+    rng = np.random.default_rng(sum(counts) + k)
+    product_case(rng, counts, n, k, okind=okind, tail=3)
+
+
 def test_product_one_expert_without_offsets():
     rng = np.random.default_rng(8)
     a, as_, w, ws = eight(rng, (37, 200), "e4m3"), scales(rng, 37, 2), eight(rng, (150, 200), "e4m3"), scales(rng, 2, 2)
