@@ -1,5 +1,6 @@
 // The experts' 8-bit products (gfx950): out[i, n] = sum_b s_b sum_{k in b}
 // a[i, k] w[e, n, k] with a scale for each block of 128 of k.
+#include "choice.h"
 #include "experts_tiles.h"
 #include "lds.h"
 #include "stages.h"
@@ -620,12 +621,10 @@ bool whole_pieces(const muon_product_args& p) {
 
 template <int FW, int FA, typename O>
 hipError_t launch(const muon_product_args& p, hipStream_t stream) {
-  const bool tiled = sizeof(O) == 2 && whole_pieces(p) && p.k > 128;
+  const bool pieces = whole_pieces(p), tiled = sizeof(O) == 2 && pieces && p.k > 128;
   const int64_t experts = p.num_experts < p.rows ? p.num_experts : p.rows, wide = (p.n + kTile - 1) / kTile;
-  // Few rows an expert: with 8 rows for each of 64 [4096, 7168] 368 us by single waves and 425 by tiles of 256,
-  // with 16 448 and 430.  Where the tiles leave CUs without one, also with more: one [4096, 7168] with 64 rows 23
-  // and 59 us, one [8192, 28672] 158 and 215, with 96 rows 250 and 220.
-  if (p.rows <= (tiled && experts * wide >= 128 ? 8 : 64) * p.num_experts && p.rows < (1 << 30)) {
+  const int64_t tiles_n = (p.n + 127) / 128;
+  if (p.rows <= most_rows_of_waves(experts * (tiled ? wide : tiles_n), tiled, pieces) * p.num_experts && p.rows < (1 << 30)) {
     // waves for all 1024 SIMDs four times over, or the blocks of k shared by up to eight
     const int64_t tiles = (p.n + 15) / 16 * experts, blocks = (p.k + 127) / 128;
     const int64_t share = tiles >= 4096 || blocks < 8 ? 1 : tiles >= 1024 || blocks < 32 ? 4 : 8;
@@ -638,7 +637,6 @@ hipError_t launch(const muon_product_args& p, hipStream_t stream) {
       return hipGetLastError();
     }
   }
-  const int64_t tiles_n = (p.n + 127) / 128;
   const int64_t most = (p.rows / 128 + (p.num_experts < p.rows ? p.num_experts : p.rows)) * tiles_n;
   ex_product<FW, FA, O><<<unsigned(most < (1 << 20) ? (most + 7) / 8 * 8 : 1 << 20), 256, 0, stream>>>(p, (uint32_t)tiles_n);
   return hipGetLastError();

@@ -120,6 +120,14 @@ def test_product_of_long_runs_among_few_rows(counts, n, k, okind):
     product_case(rng, counts, n, k, okind=okind, tail=3)
 
 
+@pytest.mark.parametrize("counts,n,k", [([600] + [0] * 14 + [3], 64, 1040), ([600] + [0] * 8 + [2], 96, 4224),
+                                        ([1, 640, 0, 320] + [0] * 12, 64, 384), ([40, 0, 513], 4200, 272)])
+def test_product_of_long_runs_to_bf16(counts, n, k):
+    """The same to bf16: waves in groups of four, of eight and single, and runs that go to tiles."""
+    rng = np.random.default_rng(sum(counts) + n + k)
+    product_case(rng, counts, n, k, tail=3)
+
+
 def test_product_one_expert_without_offsets():
     rng = np.random.default_rng(8)
     a, as_, w, ws = eight(rng, (37, 200), "e4m3"), scales(rng, 37, 2), eight(rng, (150, 200), "e4m3"), scales(rng, 2, 2)
