@@ -600,9 +600,11 @@ template <int FW, int FA, typename O, int KS>
 hipError_t launch_few(const muon_product_args& p, hipStream_t stream) {
   constexpr int TILES = KS > 4 ? 1 : 4 / KS;
   const int64_t x = (p.n + TILES * 16 - 1) / (TILES * 16);
-  // a run of most of the rows goes to up to four workgroups, 64 rows each in turn: 512 rows with one of 64
-  // [4096, 7168] 288 us, 526 by one; 8 rows with each 396 and 397, 96 rows with 50 of them 278 and 276
-  const int64_t z = (p.rows + 63) / 64;
+  // A run of most of the rows goes to up to four workgroups, 64 rows each in turn: 192 rows with one of 64 [4096,
+  // 7168] 141 us, 198 by one; to fp32 1024 rows with one of 128 [2048, 4096] 232 and 667.  Even runs pay for
+  // workgroups that find no rows: 8 rows for each of 64 [4096, 7168] to fp32 582 and 527.  Two turns are one
+  // workgroup's: 128 rows with one of eight [4096, 4096] to fp32 35 by one, 44 by two, 16 with each 60 and 70.
+  const int64_t z = p.rows <= 128 ? 1 : (p.rows + 63) / 64;
   ex_product_few<FW, FA, O, KS><<<dim3(unsigned(x < (1 << 20) ? x : 1 << 20), unsigned(p.num_experts), unsigned(z < 4 ? z : 4)),
                                  KS > 4 ? 64 * KS : 256, 0, stream>>>(p);
   return hipGetLastError();
