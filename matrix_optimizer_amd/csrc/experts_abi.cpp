@@ -36,7 +36,7 @@ void stack(Buffers& b, const void* p, int64_t batch, int64_t rows, int64_t cols,
   }
 }
 
-muon_status check_groups(int64_t rows, int64_t experts, const int32_t* offsets) {
+muon_status check_groups(int64_t experts, const int32_t* offsets) {
   if (experts < 1) return MUON_ERR_INVALID_ARG;
   if (experts > MUON_ROUTE_MAX_EXPERTS) return MUON_ERR_UNSUPPORTED;
   if (!offsets && experts != 1) return MUON_ERR_INVALID_ARG;
@@ -195,7 +195,7 @@ muon_status muon_expert_product(const muon_product_args* a, void* stream) {
   muon_status st = check_dims(a->rows, a->k);
   if (st != MUON_OK) return st;
   if ((st = check_dims(0, a->n)) != MUON_OK) return st;
-  if ((st = check_groups(a->rows, a->num_experts, a->offsets)) != MUON_OK) return st;
+  if ((st = check_groups(a->num_experts, a->offsets)) != MUON_OK) return st;
   if (!eight_bit(a->a_dtype) || !eight_bit(a->w_dtype) || !valid_dtype(a->out_dtype)) return MUON_ERR_INVALID_ARG;
   if (too_many(a->num_experts, a->n, a->k)) return MUON_ERR_UNSUPPORTED;
   // tiles are numbered in 32 bits
@@ -234,7 +234,7 @@ muon_status muon_expert_weight_grad(const muon_weight_grad_args* a, void* worksp
   size_t need = 0;
   muon_status st = muon_expert_weight_grad_workspace_bytes(a->rows, a->num_experts, a->n, a->k, &need);
   if (st != MUON_OK) return st;
-  if ((st = check_groups(a->rows, a->num_experts, a->offsets)) != MUON_OK) return st;
+  if ((st = check_groups(a->num_experts, a->offsets)) != MUON_OK) return st;
   if (!valid_dtype(a->dw_dtype)) return MUON_ERR_INVALID_ARG;
   if (workspace_bytes < need) return MUON_ERR_WORKSPACE_TOO_SMALL;
   Buffers b;

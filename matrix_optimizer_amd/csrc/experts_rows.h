@@ -15,15 +15,13 @@ struct RowLayout {
 
 // Lanes enough for a row's chunks, from 16 (a group of 128 columns) to 256; few rows are split over
 // workgroups along their columns as well, until there are about two for each of the 256 CUs.
-inline RowLayout row_layout(int64_t rows, int64_t chunks, bool may_split = true) {
+inline RowLayout row_layout(int64_t rows, int64_t chunks) {
   RowLayout l{4, 1, 1};
   while (l.log_lanes < 8 && (int64_t(1) << l.log_lanes) < chunks) ++l.log_lanes;
   const int64_t per = 256 >> l.log_lanes, groups = (rows + per - 1) / per, most = 1 << 20;
   l.gx = unsigned(groups < most ? groups : most);
-  if (may_split) {
-    const int64_t steps = (chunks + 255) / 256, want = groups >= 512 ? 1 : (512 + groups - 1) / groups;
-    l.gy = unsigned(want < steps ? want : steps);
-  }
+  const int64_t steps = (chunks + 255) / 256, want = groups >= 512 ? 1 : (512 + groups - 1) / groups;
+  l.gy = unsigned(want < steps ? want : steps);
   return l;
 }
 

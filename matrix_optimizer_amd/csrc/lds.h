@@ -75,17 +75,11 @@ __device__ __forceinline__ void lds_dma16(const u32x4& buffer, uint32_t voff, ui
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                :: "v"(voff), "s"(buffer), "s"(sl) : "memory", "m0");
 }
+// 4 bytes per lane, to lds_addr + 4 lane.
 __device__ __forceinline__ void lds_dma4(const u32x4& buffer, uint32_t voff, uint32_t lds_addr) {
   const uint32_t sl = __builtin_amdgcn_readfirstlane(lds_addr);
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
                :: "v"(voff), "s"(buffer), "s"(sl) : "memory", "m0");
-}
-// The same with 4 bytes per lane, to lds_addr + 4 lane.
-__device__ __forceinline__ void lds_dma4(const void* base, uint32_t voff, uint32_t lds_addr) {
-  const uint64_t sb = (uint64_t)uniform64((int64_t)(uintptr_t)base);
-  const uint32_t sl = __builtin_amdgcn_readfirstlane(lds_addr);
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
-               :: "v"(voff), "s"(sb), "s"(sl) : "memory", "m0");
 }
 #pragma clang diagnostic pop
 
