@@ -81,10 +81,11 @@ muon_status muon_dropout(int64_t rows, int64_t cols, const void* x, int64_t x_st
  * 8-bit y: per row, groups of `group` columns (32, 64 or 128; 0 = the whole
  * row) share a scale; scales[r * scales_stride + g] = max |y| over the group
  * times 1 / FMAX in fp32, 1 if that maximum is 0, at least 2^-126; the stored
- * value is the fp32 quotient y / scale by that scale, rounded to nearest even,
- * at most FMAX in magnitude.  A NaN in y is stored as a NaN and does not enter
- * the maximum; an infinity makes the group's scale infinite and the infinite
- * elements NaN. */
+ * value is the quotient y / scale by that scale, rounded to nearest even, at
+ * most FMAX in magnitude (the fp32 quotient but for about one in a million,
+ * which is an ulp off and may so be stored as the 8-bit value next to it).  A NaN
+ * in y is stored as a NaN and does not enter the maximum; an infinity makes the
+ * group's scale infinite and the infinite elements NaN. */
 typedef struct {
   int64_t rows, cols;
   const void* x;        int64_t x_stride;

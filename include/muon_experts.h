@@ -36,10 +36,11 @@
  * 8-bit values: groups of 128 columns of a row (rows) or blocks of 128 x 128
  * (matrices), the last ones shorter, share an fp32 scale:
  * scale = max |v| / FMAX as an fp32 quotient, 1 if that maximum is 0, at
- * least 2^-126; the stored value is the fp32 quotient v / scale, rounded to
- * nearest even.  A NaN is stored as a NaN and does not enter the maximum; an
- * infinity makes the scale infinite, its finite values 0 and its infinite
- * ones NaN.  muon_norm_forward with group = 128 writes rows of this layout.
+ * least 2^-126; the stored value is the quotient v / scale, rounded to nearest
+ * even.  The quotient is the fp32 one but for about one in a million, which is
+ * an ulp off and may so be stored as the 8-bit value next to it.  A NaN is
+ * stored as a NaN and does not enter the maximum; an infinity makes the scale
+ * infinite, its finite values 0 and its infinite ones NaN.  muon_norm_forward with group = 128 writes rows of this layout.
  */
 #ifndef LIBMUON_MUON_EXPERTS_H
 #define LIBMUON_MUON_EXPERTS_H
@@ -91,8 +92,9 @@ muon_status muon_expert_combine(const muon_combine_args* args, void* stream);
  *   dweights[t, k] = sum over columns of dout[t] y[i] (optional, needs y),
  * and dweights = 0 for a slot without one.  Places that no slot names are
  * left as they are.  The places are distinct, as muon_route_order gives them;
- * a place named twice holds either slot's value in each column.  The gradient
- * of base is dout. */
+ * a place named twice holds either slot's value in each column (its 8-bit
+ * values and their scale need not be of the same slot).  The gradient of base
+ * is dout. */
 typedef struct {
   int64_t rows, cols, top_k, places;
   const int32_t* position;                           /* [rows, top_k], contiguous */
@@ -109,7 +111,8 @@ typedef struct {
 muon_status muon_expert_combine_backward(const muon_combine_grad_args* args, void* stream);
 
 /* Gated activation of a = [g | u], [rows, 2 cols]: y = g sigmoid(g) u, stored
- * in dtype (y) and in 8 bits with scales (y8); either or both.  `used`: an
+ * in dtype (y) and in 8 bits with scales (y8); either or both.  sigmoid(g) is an
+ * fp32 value: below g = -87 it is subnormal, with fewer digits.  `used`: an
  * optional device address of the number of rows that are in use (offsets + E);
  * rows from there on are neither read nor written. */
 typedef struct {
@@ -145,7 +148,8 @@ muon_status muon_gate_backward(const muon_gate_grad_args* args, void* stream);
  * scales [batch, ceil(rows / 128), ceil(cols / 128)], and / or transposed, qt
  * [batch, cols, rows] with scales_t [batch, ceil(cols / 128),
  * ceil(rows / 128)].  Matrices are `_matrix` elements apart (ignored for one
- * matrix), at least rows * stride for outputs; scales are contiguous. */
+ * matrix), at least (rows - 1) * stride + columns of inputs and outputs alike:
+ * they neither repeat nor interleave.  Scales are contiguous. */
 typedef struct {
   int64_t batch, rows, cols;
   const void* x;        int64_t x_stride, x_matrix;
@@ -166,7 +170,10 @@ muon_status muon_quantise_blocks(const muon_quantise_args* args, void* stream);
  * of scales outside fp32's normal range loses its digits).  With fp32 out the
  * sums over a block are fp32 sums of exact products; with bf16 out the 8-bit
  * instructions form them, which cut each of eight neighbouring products at
- * 2^-13 of the largest one's power of two.  offsets NULL: one expert, all rows.
+ * 2^-13 of the largest one's power of two: at most 7 2^-13 of the sum of the
+ * products' magnitudes, 4.4e-5 of a sum of random values in the root mean
+ * square, where the store rounds by up to 2^-8.  offsets NULL: one expert, all
+ * rows.  w's matrices are apart as in muon_quantise_blocks.
  * num_experts <= MUON_ROUTE_MAX_EXPERTS, and fewer than 2^31 pieces of out of
  * 128 x 128 in the runs. */
 typedef struct {
@@ -185,9 +192,13 @@ muon_status muon_expert_product(const muon_product_args* args, void* stream);
 /* dw[e, n, k] = sum over the places i of expert e of dy[i, n] x[i, k], bf16
  * products summed in fp32; zeros for an expert without rows.  offsets NULL:
  * one expert, all rows.  rows = 0 writes zeros.  num_experts <=
- * MUON_ROUTE_MAX_EXPERTS.  The workspace (256-byte
- * aligned) is that of muon_expert_weight_grad_workspace_bytes, 0 bytes where
- * the rows are neither split nor of odd widths; it serves one call at a time. */
+ * MUON_ROUTE_MAX_EXPERTS.  dw's matrices are apart as in muon_quantise_blocks.
+ * The workspace (256-byte aligned) is that of
+ * muon_expert_weight_grad_workspace_bytes, 0 bytes where the rows are neither
+ * split nor of odd widths; it serves one call at a time.  Its size goes by
+ * widths alone, so n and k that are multiples of 8 have no room for copies: rows
+ * of such widths at bases or strides off 16 bytes take the kernel of odd widths,
+ * which takes 2 to 2.7 times as long where there is much work. */
 typedef struct {
   int64_t rows, n, k, num_experts;
   const void* dy;       int64_t dy_stride;              /* [rows, n] bf16 */

@@ -201,7 +201,7 @@ hipError_t combine_backward_of(const muon_combine_grad_args& a, hipStream_t stre
 hipError_t run_gather(const muon_gather_args& a, hipStream_t stream) {
   const int64_t es = a.dtype == MUON_ROW_F32 ? 4 : a.dtype == MUON_ROW_BF16 ? 2 : 1;
   // Many rows: at most a wave each, with up to eight pieces a lane on their way (49152 rows of 7168 bytes
-  // and their scales 104 us; a workgroup each 128).
+  // and their scales 111 us; a workgroup each 122).
   const int64_t pairs = a.rows * a.top_k, chunks = (a.cols * es + 15) / 16;
   const RowLayout l = row_layout(pairs, pairs >= 4096 && chunks > 64 ? 64 : chunks);
   ex_gather<<<dim3(l.gx, l.gy), 256, 0, stream>>>(a, es, l.log_lanes);

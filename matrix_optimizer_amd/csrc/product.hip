@@ -17,9 +17,11 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 // neighbouring bytes form to the largest one's exponent and cuts what lies
 // 2^-13 below it (measured; so do the 8-bit instructions of 32 columns), and
 // adds the rest in fp32: sums of random values are 4.4e-5 off in the root mean
-// square, a fortieth of a bf16 output's rounding.  An fp32 output takes the
-// operands as bf16, which holds them exactly, through the bf16 instruction
-// (2.6e-8) at half the rate.
+// square, a fortieth of a bf16 output's rounding, so that 1.2 % of the outputs
+// round the other way than the exact sum and the error against 64 bits stays
+// 1.7e-3.  An fp32 output takes the operands as bf16, which holds them exactly,
+// through the bf16 instruction (2.6e-8 a block; 8e-8 in sums of 17 blocks with
+// their scales) at half the rate.
 template <int FW, int FA, typename O>
 struct Block;
 template <int FW, int FA>
@@ -232,9 +234,10 @@ __device__ __forceinline__ void store_packed8(bf16_t* p, int left, const u32x4& 
 // 49152 rows by 64 [4096, 7168] 1.57-1.61 ms, 1770 TFLOP/s of useful products at
 // 2.0 GHz; the matrix units are busy for 45 % of it.  Without any load the same
 // kernel takes 1.24 ms, with all loads from the L2 and no products 0.77, with all
-// loads and no products 1.57: it is bound by how many lines a CU has on their way,
-// 64 KB a block.  Fetching lines towards the L2 one to six blocks ahead takes their
-// place (1.57 to 1.72 ms).  With the rows in the loads' scalar offset, which the
+// loads and no products 1.57: it is bound by the time in which the 64 KB of a block
+// arrive, with one block on its way a CU (whether the cache would take more lines
+// at a time, only a loop with more stages could show).  Fetching lines towards the
+// L2 one to six blocks ahead was slower (1.57 to 1.72 ms).  With the rows in the loads' scalar offset, which the
 // hardware need not compare with a buffer's end, runs of whole tiles took 1.47 ms
 // for 1.48.  Two wave groups a quarter block apart with four barriers a
 // block took 1.80 ms, address arithmetic in the vector unit 1.72.

@@ -32,8 +32,10 @@ __device__ __forceinline__ u32x4 load8_bf16(const bf16_t* row, int64_t c, int64_
 // step: both operands lie with the rows of the sum along the slow axis, so
 // their fragments are read transposed.  Any size, stride and alignment,
 // through registers, a step ahead of the one multiplied.  777 rows of 1001 and 515
-// columns for 8 experts 16-20 us, bound by latency; 49152 rows of 1001 and 1001 for 8
-// experts took 0.52 ms and of 1024 and 1024 0.28, by loads that start at any element.
+// columns for 8 experts 18-20 us, bound by latency.  Odd widths of much work have
+// their rows copied for the kernel below; widths that are multiples of 8 in rows off
+// 16 bytes have no workspace for that and stay here: 49152 rows of 1024 and 1024 for
+// 8 experts 290 us for 140, to 64 [7168, 2048] 4.1 ms for 1.55.
 // ---------------------------------------------------------------------------
 template <typename O>
 __global__ void __launch_bounds__(256)
@@ -144,8 +146,8 @@ ex_weight_grad(muon_weight_grad_args p, Dest d, int64_t tn, int64_t tk) {
 // one exchange with the lane 32 away.
 //
 // 49152 rows to 64 [7168, 2048] bf16 1.47-1.52 ms, 930 TFLOP/s; a stage takes
-// 1.8 us (as in the 8-bit product the lines that a CU has on their way, 64 KB a
-// stage), the matrix units are busy for 47 % of it, and the 1.9 GB of results take
+// 1.8 us (as in the 8-bit product the time in which 64 KB, the one stage on its way,
+// arrive), the matrix units are busy for 47 % of it, and the 1.9 GB of results take
 // 0.24 ms that no products hide.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 256, kRows = 64, kStage = 2 * kRows * kTile * 2;
@@ -487,7 +489,7 @@ int64_t weight_grad_parts(int64_t rows, int64_t num_experts, int64_t n, int64_t 
 }
 
 // Odd widths of 2^30 products or more have their rows copied to whole pieces first: 49152 rows of 1001 and 1001
-// for 8 experts 248 us, 515 without, 4096 rows of 1001 and 515 45 and 61, 2000 of them 34 and 33, 777 24 and 15.
+// for 8 experts 230-258 us, 515 without, 4096 rows of 1001 and 515 45 and 61, 2000 of them 34 and 33, 777 24 and 15.
 int64_t weight_grad_copy_bytes(int64_t rows, int64_t num_experts, int64_t n, int64_t k) {
   if (n % 8 == 0 && k % 8 == 0) return 0;
   if (!numbers_fit(rows, num_experts, n, k, weight_grad_parts(rows, num_experts, n, k)) || rows * n < (int64_t(1) << 30) / k) return 0;

@@ -268,3 +268,12 @@ def test_binding_checks_shapes_and_types():
                  lambda: X.muon_expert_weight_grad(x, x, _t(64, 64, dtype=torch.float16))):
         with pytest.raises(TypeError):
             call()
+
+
+def test_matrices_neither_repeat_nor_interleave(mem):
+    """(rows - 1) * stride + columns is the least distance of a call's matrices, inputs' too."""
+    call = _caller("muon_quantise_blocks", X.muon_quantise_args, batch=2, rows=30, cols=64, x=mem(0), x_stride=70,
+                   x_matrix=29 * 70 + 64, q=mem(1), q_stride=70, q_matrix=29 * 70 + 64, scales=mem(2), dtype=1, q_dtype=2)
+    assert call() == HIP
+    _refused(call, (dict(x_matrix=0), dict(x_matrix=29 * 70 + 63), dict(x_stride=140, x_matrix=70),
+                    dict(q_matrix=29 * 70 + 63), dict(q_stride=140, q_matrix=70)))
