@@ -1,6 +1,6 @@
 // The gated activation between an expert's two products and its gradient
 // (gfx950), one pass over the rows each: bound by the bytes they move.  47678
-// rows of 2 x 2048 bf16 to bf16 and e4m3 131 us, 5.2 TB/s; the gradient of 49152
+// rows of 2 x 2048 bf16 to bf16 and e4m3 132-136 us, 5.1 TB/s; the gradient of 49152
 // such rows 212 us, 5.7 TB/s.
 #include <cmath>
 

@@ -232,7 +232,7 @@ __device__ __forceinline__ void store_packed8(bf16_t* p, int left, const u32x4& 
 // the next block and no wave finds itself without operands.
 //
 // 49152 rows by 64 [4096, 7168] 1.57-1.61 ms, 1770 TFLOP/s of useful products at
-// 2.0 GHz; the matrix units are busy for 45 % of it.  Without any load the same
+// 2.0 GHz; the matrix units are busy for 41-45 % of it.  Without any load the same
 // kernel takes 1.24 ms, with all loads from the L2 and no products 0.77, with all
 // loads and no products 1.57: it is bound by the time in which the 64 KB of a block
 // arrive, with one block on its way a CU (whether the cache would take more lines

@@ -147,7 +147,7 @@ ex_weight_grad(muon_weight_grad_args p, Dest d, int64_t tn, int64_t tk) {
 //
 // 49152 rows to 64 [7168, 2048] bf16 1.47-1.52 ms, 930 TFLOP/s; a stage takes
 // 1.8 us (as in the 8-bit product the time in which 64 KB, the one stage on its way,
-// arrive), the matrix units are busy for 47 % of it, and the 1.9 GB of results take
+// arrive), the matrix units are busy for 46 % of it, and the 1.9 GB of results take
 // 0.24 ms that no products hide.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 256, kRows = 64, kStage = 2 * kRows * kTile * 2;
