@@ -1,5 +1,5 @@
 """The product's choice between single waves and tiles (choice.h) where both were
-measured and one is the faster by a fifth or more, with even runs or, where
+measured and one is the faster by a sixth or more, with even runs or, where
 they are uneven, by more than that."""
 import os
 import subprocess
